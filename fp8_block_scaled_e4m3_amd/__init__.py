@@ -90,6 +90,12 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.dg_transform_sa_mn_major.restype = I
     lib.dg_check_contiguous_layout.argtypes = [P, I, I, P]
     lib.dg_check_contiguous_layout.restype = I
+    lib.dg_m_grouped_gemm_ragged_nt.argtypes = [P, L, P, P, L, P, I, I, I, I, I, P]
+    lib.dg_m_grouped_gemm_ragged_nt.restype = I
+    lib.dg_m_grouped_gemm_ragged_nn.argtypes = [P, L, P, P, L, P, I, I, I, I, I, P]
+    lib.dg_m_grouped_gemm_ragged_nn.restype = I
+    lib.dg_k_grouped_gemm_ragged_tn.argtypes = [P, L, P, L, P, P, I, I, I, I, I, I, I, P]
+    lib.dg_k_grouped_gemm_ragged_tn.restype = I
     _lib = lib
     return lib
 
@@ -369,6 +375,74 @@ def dg_check_contiguous_layout(m_indices, num_groups: int):
     return int(bad.value)
 
 
+# ---- training operators: 16-bit products grouped by expert with ragged segments
+def _half_type(*named):
+    """The 16-bit type all the tensors share, as a DG_DTYPE code (each a GPU tensor with
+    contiguous last dimension)."""
+    import torch
+    first = named[0][0]
+    for t, name, ndim in named:
+        _dev(t, name, (torch.bfloat16, torch.float16), ndim)
+        if t.dtype != first.dtype:
+            raise TypeError(f"{name} has dtype {t.dtype}, expected {first.dtype}")
+    return 1 if first.dtype == torch.bfloat16 else 2
+
+
+def _ragged_offsets(offsets, groups):
+    import torch
+    p = _dev(offsets, "offsets", (torch.int32,), 1)
+    if offsets.shape[0] != groups + 1:
+        raise ValueError(f"offsets has {offsets.shape[0]} entries, expected {groups + 1}")
+    return p
+
+
+def _ragged_with_weights(call, a, b, d, offsets, transposed, stream):
+    dt = _half_type((a, "a", 2), (b, "b", 3), (d, "d", 2))
+    groups, n, k = b.shape
+    rows, wa, wd = a.shape[0], n if transposed else k, k if transposed else n
+    if a.shape[1] != wa or tuple(d.shape) != (rows, wd):
+        raise ValueError(f"shape mismatch: a {tuple(a.shape)}, b {tuple(b.shape)}, d {tuple(d.shape)}")
+    if not b.is_contiguous():
+        raise ValueError("b must be contiguous")
+    lda, ldd = (a.stride(0), d.stride(0)) if rows > 1 else (wa, wd)
+    _check(getattr(load_library(), call)(a.data_ptr(), lda, b.data_ptr(), d.data_ptr(), ldd,
+                                         _ragged_offsets(offsets, groups), rows, n, k, groups, dt, _stream(stream)),
+           call)
+
+
+def dg_m_grouped_gemm_ragged_nt(a, b, d, offsets, stream=None) -> None:
+    """Forward product grouped by expert: d[t] = a[t] . b[g]^T for the rows t of group g,
+    which are offsets[g] .. offsets[g + 1] - 1 (int32, on the GPU; any lengths).  a [M, K],
+    b [G, N, K], d [M, N], all bfloat16 or all float16; rows outside every segment are left."""
+    _ragged_with_weights("dg_m_grouped_gemm_ragged_nt", a, b, d, offsets, False, stream)
+
+
+def dg_m_grouped_gemm_ragged_nn(a, b, d, offsets, stream=None) -> None:
+    """Gradient of the forward product's input: d[t] = a[t] . b[g], with a [M, N] the gradient
+    of its output, b [G, N, K] its weights, d [M, K]."""
+    _ragged_with_weights("dg_m_grouped_gemm_ragged_nn", a, b, d, offsets, True, stream)
+
+
+def dg_k_grouped_gemm_ragged_tn(a, b, d, offsets, accumulate=False, stream=None) -> None:
+    """Gradient of the forward product's weights: d[g] = sum over the group's rows t of
+    a[t]^T b[t], with a [M, N] the gradient of its output, b [M, K] its input, d [G, N, K] of
+    their type or float32; ``accumulate`` adds to what d holds (otherwise a group without
+    rows gets zeros)."""
+    import torch
+    dt = _half_type((a, "a", 2), (b, "b", 2))
+    _dev(d, "d", (a.dtype, torch.float32), 3)
+    (rows, n), (groups, dn, k) = a.shape, d.shape
+    if dn != n or tuple(b.shape) != (rows, k):
+        raise ValueError(f"shape mismatch: a {tuple(a.shape)}, b {tuple(b.shape)}, d {tuple(d.shape)}")
+    if not d.is_contiguous():
+        raise ValueError("d must be contiguous")
+    lda, ldb = (a.stride(0), b.stride(0)) if rows > 1 else (n, k)
+    _check(load_library().dg_k_grouped_gemm_ragged_tn(a.data_ptr(), lda, b.data_ptr(), ldb, d.data_ptr(),
+                                                      _ragged_offsets(offsets, groups), rows, n, k, groups, dt,
+                                                      0 if d.dtype == torch.float32 else dt, int(bool(accumulate)),
+                                                      _stream(stream)), "dg_k_grouped_gemm_ragged_tn")
+
+
 # ---- the README's Python names ("deepseek-ai/deepgemm: clean and efficient FP8 GEMM
 # kernels", usage and utility paragraphs): the same calls, with operands passed as
 # (data, scale) pairs and the LHS scales as the README lays them out -- a [M, K/128]
@@ -500,6 +574,7 @@ __all__ = [
     "dg_quantize_fp8_1x128", "dg_quantize_fp8_128x128", "dg_quantize_fp8_1x128_fmt",
     "dg_quantize_fp8_128x128_fmt", "dg_get_aligned_ld_sa", "dg_transform_sa_mn_major",
     "dg_check_contiguous_layout", "dg_plan_tiles",
+    "dg_m_grouped_gemm_ragged_nt", "dg_m_grouped_gemm_ragged_nn", "dg_k_grouped_gemm_ragged_tn",
     "dg_set_kernel_config", "dg_kernel_config_info", "dg_describe_launch",
     "gemm_fp8_fp8_bf16_nt", "m_grouped_gemm_fp8_fp8_bf16_nt_contiguous", "m_grouped_gemm_fp8_fp8_bf16_nt_masked",
     "set_num_sms", "get_num_sms", "get_m_alignment_for_contiguous_layout", "get_tma_aligned_size",

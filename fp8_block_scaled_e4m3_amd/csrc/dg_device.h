@@ -1,0 +1,67 @@
+// dg_device.h -- device helpers of the training kernels (dg_ragged.hip): raw buffer
+// descriptors, copies from a buffer straight into LDS, the waits and barrier that go
+// with them.  gfx950 only.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <type_traits>
+
+namespace dg {
+namespace dev {
+
+typedef int v4i __attribute__((ext_vector_type(4)));
+typedef int v2i __attribute__((ext_vector_type(2)));
+typedef float v4f __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) void lds_void;
+typedef __attribute__((address_space(3))) uint8_t lds_u8;
+
+// Lambdas of the kernels are always inlined: a call that stays out of line would put
+// the accumulators it captures by reference into scratch memory.
+#define DG_DEV_INLINE __attribute__((always_inline))
+
+// f(integral_constant<I>) for I = B .. E-1, unrolled at compile time.
+template <int B, int E, typename F>
+__device__ __forceinline__ void unroll(F&& f) {
+    if constexpr (B < E) {
+        f(std::integral_constant<int, B>{});
+        unroll<B + 1, E>(f);
+    }
+}
+
+// Raw buffer descriptor over `bytes` bytes from `base`: a lane whose offset lies at or
+// past the end reads zeros and touches no memory.  The callers keep every offset that is
+// meant to be inside below 2^31, so kOutside is outside of each.
+constexpr uint32_t kOutside = 0xFFFFFF00u;
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_over(const void* base, long bytes) {
+    const unsigned n = bytes <= 0 ? 0u : (bytes >= 0x7FFFFFFFl ? 0x7FFFFFFFu : (unsigned)bytes);
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, (int)n, 0x00020000);
+}
+
+// 16 bytes per lane from a buffer into LDS: lane l's land at dst + 16 l.
+template <int CPOL = 0>
+__device__ __forceinline__ void copy_to_lds16(__amdgpu_buffer_rsrc_t rs, lds_void* dst, uint32_t voff, uint32_t soff) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, dst, 16, (int)voff, (int)soff, 0, CPOL);
+}
+
+// Workgroup barrier without the memory fence of __syncthreads(), which would also drain
+// the copies that should stay in flight: the callers wait for exactly what they need
+// first.  The empty asm statements keep memory accesses on their side of it.
+__device__ __forceinline__ void barrier_only() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// At most N of this wave's vector memory operations are still outstanding.
+template <int N>
+__device__ __forceinline__ void wait_vmem() {
+    static_assert(N >= 0 && N < 64, "vmcnt range");
+    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
+}
+
+// Every LDS access of this wave has completed.
+__device__ __forceinline__ void wait_lds() { __builtin_amdgcn_s_waitcnt(0xC07F); }
+
+}  // namespace dev
+}  // namespace dg

@@ -1,0 +1,40 @@
+// dg_train.h -- shared between the training entry points (dg_train_api.cpp) and their
+// kernels (dg_ragged.hip, dg_adamw.hip).  Not part of the public ABI.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace dg {
+
+// The three products grouped by expert, as one: D[i][j] = sum_c P(i, c) Q(j, c).
+//   nt (forward)          i = token row, j = n, c = k      P = A [T][k], Q = B [g][n][k]
+//   nn (input gradient)   i = token row, j = k, c = n      P = A [T][n], Q = B [g][n][k]
+//   tn (weight gradient)  i = n, j = k, c = token row      P = A [T][n], Q = B [T][k]
+enum RaggedOp { kRaggedNT = 0, kRaggedNN = 1, kRaggedTN = 2 };
+
+// Pointers are device pointers, strides in elements.
+struct RaggedParams {
+    const uint16_t* p;  long ldp;
+    const uint16_t* q;  long ldq;  long q_gstride;   // nt, nn: elements between groups' weights
+    void* d;            long ldd;  long d_gstride;   // tn: elements between groups' gradients
+    const int* offsets;      // [groups + 1], device
+    int rows;                // token rows that exist; offsets are clamped to it
+    int groups;
+    int ni, nj, nc;          // extents of i, j, c (0 where it is the group's rows)
+    int tiles_i, tiles_j;    // tn: exact; nt, nn: tiles_i unused
+    int accumulate;          // tn: add to what D holds
+};
+
+constexpr int kMaxRaggedGroups = 1024;   // offsets are kept in LDS
+
+struct RaggedConfig {
+    int op;                  // RaggedOp
+    int half;                // 0: BF16 operands, 1: FP16
+    int out_f32;             // D in fp32 (else in the operands' type)
+    int bm, bn;              // tile of D
+    hipError_t (*launch)(const RaggedParams&, int grid, hipStream_t);
+    hipError_t (*occupancy)(int* blocks_per_cu);
+};
+const RaggedConfig* ragged_configs(int* count);   // defined in dg_ragged.hip
+
+}  // namespace dg

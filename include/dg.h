@@ -158,8 +158,8 @@ int dg_m_grouped_gemm_fp8_masked_fmt(const void* a, const float* sa, long ld_sa,
                                      int num_groups, int max_m, int n, int k,
                                      int a_fmt, int b_fmt, void* stream);
 
-/* Input element types of the casts below. */
-enum { DG_DTYPE_F32 = 0, DG_DTYPE_BF16 = 1 };
+/* Element types of the casts and of the training operators below. */
+enum { DG_DTYPE_F32 = 0, DG_DTYPE_BF16 = 1, DG_DTYPE_F16 = 2 /* training operators only */ };
 
 /* FP8 cast with per-1x128 scales -- the "prior kernel" the README's usage paragraph
  * asks for: it produces A and sA exactly as dg_gemm_fp8_nt and the grouped calls read
@@ -195,6 +195,49 @@ int dg_quantize_fp8_1x128_fmt(const void* x, int x_dtype, long ldx, int rows, in
                               void* q, long ldq, float* sa, long ld_sa, int q_fmt, void* stream);
 int dg_quantize_fp8_128x128_fmt(const void* x, int x_dtype, long ldx, int rows, int k,
                                 void* q, long ldq, float* sb, int q_fmt, void* stream);
+
+/* ---- Training operators: products grouped by expert with ragged segments ----
+ *
+ * The products that a training step runs on the experts of a mixture of experts, at the
+ * segment lengths routing gives: 16-bit operands, fp32 accumulation, no padding.  Token
+ * rows are sorted by group; offsets [num_groups + 1] int32 (device) gives group g the rows
+ * [offsets[g], offsets[g+1]), of any length, zero included.
+ *   dtype  DG_DTYPE_BF16 or DG_DTYPE_F16, of a and b, and of d unless said otherwise.
+ *   b      [num_groups][n][k] in the two calls with weights: the same weights, as the
+ *          framework's other calls take them, serve the forward pass and its gradient.
+ * Offsets are read on the device only.  They are clamped to [0, m_total] and an entry below
+ * an earlier one counts as that one, so no offsets lead outside the operands; rows of a
+ * and d outside every segment (before the first, after the last) are not read and not
+ * written.  A row that is NaN or infinite in one group's rows does not reach another's.
+ * Requirements: n % 8 == 0, k % 8 == 0, num_groups <= 1024, n, k and leading dimensions
+ * below 2^22 (else DG_ERR_UNSUPPORTED); a, b, d 16-byte aligned and leading dimensions
+ * multiples of 8 (else DG_ERR_MISALIGNED); leading dimensions at least the width, non-null
+ * pointers for non-empty problems (else DG_ERR_INVALID_ARG).  The contraction must not be
+ * empty in the calls with weights (DG_ERR_UNSUPPORTED).  d must not overlap a or b.
+ * dg_set_num_cus caps these kernels as it does the FP8 ones.
+ *
+ * Forward: d[t][n] = sum_k a[t][k] b[g(t)][n][k].
+ *   a [m_total][lda >= k]    d [m_total][ldd >= n] */
+int dg_m_grouped_gemm_ragged_nt(const void* a, long lda, const void* b, void* d, long ldd,
+                                const int* offsets, int m_total, int n, int k, int num_groups,
+                                int dtype, void* stream);
+
+/* Gradient of the forward call's input, a being the gradient of its output:
+ * d[t][k] = sum_n a[t][n] b[g(t)][n][k].
+ *   a [m_total][lda >= n]    d [m_total][ldd >= k] */
+int dg_m_grouped_gemm_ragged_nn(const void* a, long lda, const void* b, void* d, long ldd,
+                                const int* offsets, int m_total, int n, int k, int num_groups,
+                                int dtype, void* stream);
+
+/* Gradient of the forward call's weights, a being the gradient of its output and b its
+ * input: d[g][n][k] = sum over g's rows t of a[t][n] b[t][k].
+ *   a [m_total][lda >= n]    b [m_total][ldb >= k]    d [num_groups][n][k]
+ *   d_dtype     dtype, or DG_DTYPE_F32
+ *   accumulate  1: the sums are added to what d holds (in fp32, rounded once to d's type);
+ *               0: they replace it, and a group without rows gets zeros. */
+int dg_k_grouped_gemm_ragged_tn(const void* a, long lda, const void* b, long ldb, void* d,
+                                const int* offsets, int m_total, int n, int k, int num_groups,
+                                int dtype, int d_dtype, int accumulate, void* stream);
 
 /* Leading dimension (in floats) that an MN-major sA of `rows` rows needs: rows rounded
  * up to a multiple of 4, so that every K block's scales start 16-byte aligned (the
