@@ -96,6 +96,13 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.dg_m_grouped_gemm_ragged_nn.restype = I
     lib.dg_k_grouped_gemm_ragged_tn.argtypes = [P, L, P, L, P, P, I, I, I, I, I, I, I, P]
     lib.dg_k_grouped_gemm_ragged_tn.restype = I
+    D = ctypes.c_double
+    lib.dg_adamw_plan_bytes.argtypes = [P, I]
+    lib.dg_adamw_plan_bytes.restype = L
+    lib.dg_adamw_plan.argtypes = [P, I, P, L]
+    lib.dg_adamw_plan.restype = I
+    lib.dg_adamw_step.argtypes = [P, I, L, L, D, D, D, D, D, P, P]
+    lib.dg_adamw_step.restype = I
     _lib = lib
     return lib
 
@@ -443,6 +450,104 @@ def dg_k_grouped_gemm_ragged_tn(a, b, d, offsets, accumulate=False, stream=None)
                                                       _stream(stream)), "dg_k_grouped_gemm_ragged_tn")
 
 
+# ---- training operators: an AdamW step over many tensors at once
+DG_STATE_F32, DG_STATE_E4M3 = 0, 1
+
+
+class _AdamwTensor(ctypes.Structure):
+    """dg_adamw_tensor of dg.h."""
+    _fields_ = [(f, ctypes.c_void_p) for f in ("param", "grad", "exp_avg", "exp_avg_sq", "exp_avg_scale",
+                                               "exp_avg_sq_scale", "copy")] + [
+        ("numel", ctypes.c_long), ("param_dtype", ctypes.c_int), ("grad_dtype", ctypes.c_int),
+        ("copy_dtype", ctypes.c_int), ("state_format", ctypes.c_int)]
+
+
+class AdamWPlan:
+    """The table of a parameter group's tensors on the GPU (dg_adamw_plan).  It names the tensors by
+    address: it holds on to them, and a tensor that is replaced needs a new plan."""
+
+    def __init__(self, table, count, tensors):
+        self.table, self.count, self.tensors = table, count, tensors
+
+
+def _flat_dev(t, name, dtypes, numel, device):
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"{name} must be on {device}, the GPU of the first parameter")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.numel() != numel:
+        raise ValueError(f"{name} has {t.numel()} elements, expected {numel}")
+    return t.data_ptr()
+
+
+def dg_adamw_plan_bytes(tensors) -> int:
+    """Bytes of the table of ``tensors`` (a ctypes array of dg_adamw_tensor)."""
+    v = int(load_library().dg_adamw_plan_bytes(tensors, len(tensors)))
+    if v < 0:
+        raise DGError(v, "dg_adamw_plan_bytes")
+    return v
+
+
+def dg_adamw_plan(params, grads, exp_avgs, exp_avg_sqs, exp_avg_scales=None, exp_avg_sq_scales=None,
+                  copies=None) -> AdamWPlan:
+    """Lay out the table of a parameter group once, for dg_adamw_step.  Lists of tensors, one entry
+    per parameter: params float32 or bfloat16; grads float32, bfloat16 or float16; the moments
+    float32, or (with both lists of scales, float32 [ceil(numel / 128)]) float8_e4m3fn or uint8
+    codes; copies bfloat16 or float16, or None.  All contiguous and on one GPU."""
+    import torch
+    count = len(params)
+    fp8 = exp_avg_scales is not None
+    if fp8 != (exp_avg_sq_scales is not None):
+        raise ValueError("8-bit states need the scales of both moments")
+    lists = {"grads": grads, "exp_avgs": exp_avgs, "exp_avg_sqs": exp_avg_sqs, "exp_avg_scales": exp_avg_scales,
+             "exp_avg_sq_scales": exp_avg_sq_scales, "copies": copies}
+    for name, x in lists.items():
+        if x is not None and len(x) != count:
+            raise ValueError(f"{name} has {len(x)} tensors, expected {count}")
+    codes = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+    state = _fp8_types() if fp8 else (torch.float32,)
+    table = (_AdamwTensor * count)()
+    for i, (t, p) in enumerate(zip(table, params)):
+        if not isinstance(p, torch.Tensor) or not p.is_cuda:
+            raise ValueError("parameters must be GPU tensors")
+        n, dev = p.numel(), params[0].device
+        blocks = -(-n // 128)
+        t.param = _flat_dev(p, "param", (torch.float32, torch.bfloat16), n, dev)
+        t.grad = _flat_dev(grads[i], "grad", tuple(codes), n, dev)
+        t.exp_avg = _flat_dev(exp_avgs[i], "exp_avg", state, n, dev)
+        t.exp_avg_sq = _flat_dev(exp_avg_sqs[i], "exp_avg_sq", state, n, dev)
+        if fp8:
+            t.exp_avg_scale = _flat_dev(exp_avg_scales[i], "exp_avg_scale", _f32(), blocks, dev)
+            t.exp_avg_sq_scale = _flat_dev(exp_avg_sq_scales[i], "exp_avg_sq_scale", _f32(), blocks, dev)
+        if copies is not None:
+            t.copy = _flat_dev(copies[i], "copy", (torch.bfloat16, torch.float16), n, dev)
+            t.copy_dtype = codes[copies[i].dtype]
+        t.numel, t.param_dtype, t.grad_dtype = n, codes[p.dtype], codes[grads[i].dtype]
+        t.state_format = DG_STATE_E4M3 if fp8 else DG_STATE_F32
+    host = torch.empty(dg_adamw_plan_bytes(table), dtype=torch.uint8)
+    _check(load_library().dg_adamw_plan(table, count, host.data_ptr(), host.numel()), "dg_adamw_plan")
+    keep = (list(params), *(list(x) for x in lists.values() if x is not None))
+    return AdamWPlan(host.to(params[0].device) if count else host, count, keep)
+
+
+def dg_adamw_step(plan, step, lr, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.01, grad_scale=None,
+                  stream=None) -> None:
+    """One AdamW step (the ``step``-th, from 1) of every tensor of the plan, in one launch;
+    ``grad_scale`` is an optional float32 GPU scalar that multiplies the gradients."""
+    if grad_scale is not None:
+        _dev(grad_scale.view(-1), "grad_scale", _f32(), 1)
+        if grad_scale.numel() != 1:
+            raise ValueError("grad_scale must hold one value")
+    _check(load_library().dg_adamw_step(plan.table.data_ptr(), plan.count, plan.table.numel(), step, lr, beta1, beta2,
+                                        eps, weight_decay, None if grad_scale is None else grad_scale.data_ptr(),
+                                        _stream(stream)), "dg_adamw_step")
+
+
 # ---- the README's Python names ("deepseek-ai/deepgemm: clean and efficient FP8 GEMM
 # kernels", usage and utility paragraphs): the same calls, with operands passed as
 # (data, scale) pairs and the LHS scales as the README lays them out -- a [M, K/128]
@@ -575,6 +680,7 @@ __all__ = [
     "dg_quantize_fp8_128x128_fmt", "dg_get_aligned_ld_sa", "dg_transform_sa_mn_major",
     "dg_check_contiguous_layout", "dg_plan_tiles",
     "dg_m_grouped_gemm_ragged_nt", "dg_m_grouped_gemm_ragged_nn", "dg_k_grouped_gemm_ragged_tn",
+    "AdamWPlan", "DG_STATE_F32", "DG_STATE_E4M3", "dg_adamw_plan_bytes", "dg_adamw_plan", "dg_adamw_step",
     "dg_set_kernel_config", "dg_kernel_config_info", "dg_describe_launch",
     "gemm_fp8_fp8_bf16_nt", "m_grouped_gemm_fp8_fp8_bf16_nt_contiguous", "m_grouped_gemm_fp8_fp8_bf16_nt_masked",
     "set_num_sms", "get_num_sms", "get_m_alignment_for_contiguous_layout", "get_tma_aligned_size",

@@ -1,0 +1,224 @@
+// dg_adamw.hip -- gfx950 kernel of an AdamW step over many tensors at once, with
+// optimizer states in fp32 or in 8 bits (dg.h).
+//
+//   g = grad [* grad_scale];  m = b1 m + (1 - b1) g;  v = b2 v + (1 - b2) g^2
+//   p = p (1 - lr wd) - lr / (1 - b1^t) * m / (sqrt(v) / sqrt(1 - b2^t) + eps)
+//
+// All of it in fp32, every operation rounded once and none contracted into a fused
+// multiply-add, so that the 8-bit codes are a deterministic function of the inputs (a sum
+// that is one ulp off can cross a rounding decision of the code).
+//
+// 8-bit states: 128 consecutive elements of a tensor share an fp32 scale, codes are E4M3
+// as the casts write them (scale = fp32(amax / 448), code = E4M3 of fp32(x / scale)).
+// m is held as it is, v as its root: E4M3 spans 2^18, which roots of a block's second
+// moments stay within where the moments themselves would not.  A root that is not zero
+// gets at least the smallest code: rounded to zero, it would leave m / eps in the next step.
+//
+// A workgroup takes one chunk of one tensor (the plan's table says which), a thread eight
+// consecutive elements, so that every access is 8 to 32 bytes per lane and a block of 128
+// is 16 lanes.  Each byte of the state moves once each way.
+#include "dg_cast_math.h"
+#include "dg_train.h"
+#include "../../include/dg.h"
+
+namespace dg {
+
+namespace {
+
+using namespace castmath;
+
+constexpr int kEach = 8;                    // elements of a thread
+constexpr int kThreads = kAdamwChunk / kEach;
+typedef float f4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+typedef float f2 __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ float half_bits_to_float(uint32_t h) {
+    return (float)__builtin_bit_cast(_Float16, (uint16_t)h);
+}
+__device__ __forceinline__ float load_as_float(const void* p, long i, int type) {
+    if (type == DG_DTYPE_F32) return static_cast<const float*>(p)[i];
+    const uint32_t h = static_cast<const uint16_t*>(p)[i];
+    return type == DG_DTYPE_BF16 ? __uint_as_float(h << 16) : half_bits_to_float(h);
+}
+__device__ __forceinline__ uint32_t bits16(float x, int type) {
+    if (type == DG_DTYPE_BF16) return __builtin_bit_cast(uint16_t, (__bf16)x);
+    return __builtin_bit_cast(uint16_t, (_Float16)x);
+}
+
+// eight elements from i (a multiple of eight), of which `n` exist (the rest become 0)
+__device__ __forceinline__ void load8(float* x, const void* p, long i, int n, int type) {
+    if (n == kEach) {
+        if (type == DG_DTYPE_F32) {
+            const f4* q = reinterpret_cast<const f4*>(static_cast<const float*>(p) + i);
+            const f4 a = q[0], b = q[1];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) { x[e] = a[e]; x[4 + e] = b[e]; }
+        } else {
+            const u4 w = *reinterpret_cast<const u4*>(static_cast<const uint16_t*>(p) + i);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                x[2 * e] = type == DG_DTYPE_BF16 ? __uint_as_float(w[e] << 16) : half_bits_to_float(w[e] & 0xFFFF);
+                x[2 * e + 1] = type == DG_DTYPE_BF16 ? __uint_as_float(w[e] & 0xFFFF0000u) : half_bits_to_float(w[e] >> 16);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) x[e] = e < n ? load_as_float(p, i + e, type) : 0.f;
+    }
+}
+__device__ __forceinline__ void store8(const float* x, void* p, long i, int n, int type) {
+    if (n == kEach) {
+        if (type == DG_DTYPE_F32) {
+            f4* q = reinterpret_cast<f4*>(static_cast<float*>(p) + i);
+            q[0] = f4{x[0], x[1], x[2], x[3]};
+            q[1] = f4{x[4], x[5], x[6], x[7]};
+        } else {
+            u4 w;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[e] = bits16(x[2 * e], type) | (bits16(x[2 * e + 1], type) << 16);
+            *reinterpret_cast<u4*>(static_cast<uint16_t*>(p) + i) = w;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < kEach; ++e)
+            if (e < n) {
+                if (type == DG_DTYPE_F32) static_cast<float*>(p)[i + e] = x[e];
+                else static_cast<uint16_t*>(p)[i + e] = (uint16_t)bits16(x[e], type);
+            }
+    }
+}
+
+// E4M3 codes times their block's scale
+__device__ __forceinline__ void load8_fp8(float* x, const void* p, long i, int n, float scale) {
+    const uint8_t* q = static_cast<const uint8_t*>(p) + i;
+    u2 w = {0u, 0u};
+    if (n == kEach) {
+        w = *reinterpret_cast<const u2*>(q);
+    } else {
+        for (int e = 0; e < n; ++e) w[e >> 2] |= (uint32_t)q[e] << (8 * (e & 3));
+    }
+#pragma unroll
+    for (int d = 0; d < 2; ++d) {
+        const f2 lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[d], false), hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[d], true);
+        x[4 * d] = lo.x * scale;
+        x[4 * d + 1] = lo.y * scale;
+        x[4 * d + 2] = hi.x * scale;
+        x[4 * d + 3] = hi.y * scale;
+    }
+}
+
+// maximum over each aligned group of 16 lanes of non-negative values that are not NaN
+// (they order like their bits), through the vector ALU's lane swaps
+template <int CTRL>
+__device__ __forceinline__ int swap_max(int x) {
+    const int o = __builtin_amdgcn_update_dpp(0, x, CTRL, 0xF, 0xF, false);
+    return o > x ? o : x;
+}
+__device__ __forceinline__ float max_of_16(float v) {
+    int b = __float_as_int(v);
+    b = swap_max<0xB1>(b);      // quad_perm [1,0,3,2]
+    b = swap_max<0x4E>(b);      // quad_perm [2,3,0,1]
+    b = swap_max<0x141>(b);     // row_half_mirror
+    b = swap_max<0x140>(b);     // row_mirror
+    return __int_as_float(b);
+}
+
+// Codes and scale of a block whose 16 lanes hold eight elements each.  ROOT: roots, of
+// which one that is not zero gets a code that is not zero.  (The codes of elements that do
+// not exist are not stored; as zeros they do not raise the maximum.)
+template <bool ROOT>
+__device__ __forceinline__ void store8_fp8(const float* x, void* p, float* scale_at, long i, int n) {
+    float amax = 0.f;
+    bool nan = false;
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+        const float a = fabsf(x[e]);
+        amax = a > amax ? a : amax;             // a NaN never raises it
+        nan |= x[e] != x[e];
+    }
+    amax = max_of_16(amax);
+    const float scale = block_scale<0>(amax);
+    u2 w;
+    if (__ballot(!(fast_scale(scale) && !nan)) == 0) {      // the whole wave takes one path
+        const float r = rcp_exact(scale);
+#pragma unroll
+        for (int d = 0; d < 2; ++d) {
+            int c = Fp8Out<0>::pack<false>(div_fast(x[4 * d], scale, r), div_fast(x[4 * d + 1], scale, r), 0);
+            w[d] = (uint32_t)Fp8Out<0>::pack<true>(div_fast(x[4 * d + 2], scale, r), div_fast(x[4 * d + 3], scale, r), c);
+        }
+    } else {
+#pragma unroll
+        for (int d = 0; d < 2; ++d) {
+            w[d] = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[d] |= e4m3_code(x[4 * d + e] / scale) << (8 * e);
+        }
+    }
+    if constexpr (ROOT) {
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) {
+            const uint32_t at = 8 * (e & 3);
+            if (x[e] > 0.f && ((w[e >> 2] >> at) & 0xFF) == 0) w[e >> 2] |= 1u << at;
+        }
+    }
+    uint8_t* q = static_cast<uint8_t*>(p) + i;
+    if (n == kEach) {
+        *reinterpret_cast<u2*>(q) = w;
+    } else {
+        for (int e = 0; e < n; ++e) q[e] = (uint8_t)(w[e >> 2] >> (8 * (e & 3)));
+    }
+    if (n > 0 && threadIdx.x % 16 == 0) *scale_at = scale;
+}
+
+__global__ void __launch_bounds__(kThreads) adamw_kernel(const AdamwParams a) {
+#pragma clang fp contract(off)
+    const AdamwEntry& t = a.entries[a.tensor_of[blockIdx.x]];
+    const long i = (long)((int)blockIdx.x - t.first_chunk) * kAdamwChunk + threadIdx.x * kEach;
+    const long left = t.numel - i;
+    const int n = left >= kEach ? kEach : (left > 0 ? (int)left : 0);
+    float g[kEach], p[kEach], m[kEach], v[kEach], root[kEach];
+    load8(g, t.grad, i, n, t.grad_type);
+    load8(p, t.param, i, n, t.param_type);
+    if (t.fp8) {
+        const float sm = n > 0 ? t.m_scale[i / 128] : 0.f, sv = n > 0 ? t.v_scale[i / 128] : 0.f;
+        load8_fp8(m, t.m, i, n, sm);
+        load8_fp8(v, t.v, i, n, sv);
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) v[e] = v[e] * v[e];
+    } else {
+        load8(m, t.m, i, n, DG_DTYPE_F32);
+        load8(v, t.v, i, n, DG_DTYPE_F32);
+    }
+    if (a.grad_scale) {
+        const float s = *a.grad_scale;
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) g[e] = g[e] * s;
+    }
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+        m[e] = m[e] * a.beta1 + g[e] * a.one_minus_beta1;
+        v[e] = v[e] * a.beta2 + (g[e] * g[e]) * a.one_minus_beta2;
+        root[e] = __builtin_sqrtf(v[e]);
+        p[e] = p[e] * a.decay - (m[e] / (root[e] * a.root2 + a.eps)) * a.size;
+    }
+    store8(p, t.param, i, n, t.param_type);
+    if (t.copy) store8(p, t.copy, i, n, t.copy_type);
+    if (t.fp8) {
+        store8_fp8<false>(m, t.m, t.m_scale + i / 128, i, n);
+        store8_fp8<true>(root, t.v, t.v_scale + i / 128, i, n);
+    } else {
+        store8(m, t.m, i, n, DG_DTYPE_F32);
+        store8(v, t.v, i, n, DG_DTYPE_F32);
+    }
+}
+
+}  // namespace
+
+hipError_t launch_adamw(const AdamwParams& p, long chunks, hipStream_t stream) {
+    hipLaunchKernelGGL(adamw_kernel, dim3((unsigned)chunks), dim3(kThreads), 0, stream, p);
+    return hipGetLastError();
+}
+
+}  // namespace dg

@@ -37,4 +37,31 @@ struct RaggedConfig {
 };
 const RaggedConfig* ragged_configs(int* count);   // defined in dg_ragged.hip
 
+// ---- AdamW ----
+// One tensor of a plan's table, as the kernel reads it (device memory).
+struct AdamwEntry {
+    void* param;
+    const void* grad;
+    void* m;
+    void* v;
+    float* m_scale;          // 8-bit states, else null
+    float* v_scale;
+    void* copy;              // or null
+    long numel;
+    int first_chunk;         // chunks of the tensors before it
+    uint8_t param_type, grad_type, copy_type, fp8;   // DG_DTYPE_*
+};
+
+struct AdamwParams {
+    const AdamwEntry* entries;
+    const int* tensor_of;    // tensor of each chunk
+    const float* grad_scale; // device, or null
+    float beta1, one_minus_beta1, beta2, one_minus_beta2;
+    float root2;             // 1 / sqrt(1 - beta2^t)
+    float eps, decay, size;  // 1 - lr wd;  lr / (1 - beta1^t)
+};
+
+constexpr int kAdamwChunk = 2048;        // elements of a workgroup: whole 128-element blocks
+hipError_t launch_adamw(const AdamwParams& p, long chunks, hipStream_t stream);   // dg_adamw.hip
+
 }  // namespace dg

@@ -1,12 +1,15 @@
 // dg_train_api.cpp -- C ABI of the training operators (dg.h): argument validation,
-// choice of the tile and launch of the kernels in dg_ragged.hip.  Host code only; like
+// choice of the tile, layout of the AdamW table and launch of the kernels in
+// dg_ragged.hip and dg_adamw.hip.  Host code only; like
 // dg_api.cpp it never touches device memory, so every call is asynchronous on the
 // caller's stream and graph-capturable.
 #include <hip/hip_runtime.h>
 
 #include <atomic>
 #include <climits>
+#include <cmath>
 #include <cstdint>
+#include <cstring>
 
 #include "../../include/dg.h"
 #include "dg_train.h"
@@ -76,6 +79,41 @@ int check_ragged(const void* a, long lda, int width_a, const void* b, long ldb, 
     if (!aligned(a, 16) || !aligned(b, 16) || !aligned(d, 16) || lda % 8 || ldb % 8 || ldd % 8 || !aligned(offsets, 4))
         return DG_ERR_MISALIGNED;
     return DG_OK;
+}
+
+// Checks one tensor of an AdamW plan and counts its chunks.
+int check_adamw(const dg_adamw_tensor& t, long* chunks) {
+    *chunks = 0;
+    if (t.numel < 0) return DG_ERR_INVALID_ARG;
+    if (t.param_dtype != DG_DTYPE_F32 && t.param_dtype != DG_DTYPE_BF16) return DG_ERR_INVALID_ARG;
+    if (t.grad_dtype != DG_DTYPE_F32 && t.grad_dtype != DG_DTYPE_BF16 && t.grad_dtype != DG_DTYPE_F16)
+        return DG_ERR_INVALID_ARG;
+    if (t.copy && t.copy_dtype != DG_DTYPE_BF16 && t.copy_dtype != DG_DTYPE_F16) return DG_ERR_INVALID_ARG;
+    if (t.state_format != DG_STATE_F32 && t.state_format != DG_STATE_E4M3) return DG_ERR_INVALID_ARG;
+    if (t.numel == 0) return DG_OK;
+    if (!t.param || !t.grad || !t.exp_avg || !t.exp_avg_sq) return DG_ERR_INVALID_ARG;
+    const bool fp8 = t.state_format == DG_STATE_E4M3;
+    if (fp8 && (!t.exp_avg_scale || !t.exp_avg_sq_scale)) return DG_ERR_INVALID_ARG;
+    if (t.numel > LONG_MAX / 8) return DG_ERR_UNSUPPORTED;
+    if (!aligned(t.param, 16) || !aligned(t.grad, 16) || !aligned(t.copy, 16) || !aligned(t.exp_avg, fp8 ? 8 : 16) ||
+        !aligned(t.exp_avg_sq, fp8 ? 8 : 16) || !aligned(t.exp_avg_scale, 4) || !aligned(t.exp_avg_sq_scale, 4))
+        return DG_ERR_MISALIGNED;
+    *chunks = t.numel / dg::kAdamwChunk + (t.numel % dg::kAdamwChunk != 0);
+    return DG_OK;
+}
+
+// Chunks of all tensors, or a negative status.
+long count_chunks(const dg_adamw_tensor* tensors, int count) {
+    if (count < 0 || (count > 0 && !tensors)) return DG_ERR_INVALID_ARG;
+    long total = 0;
+    for (int i = 0; i < count; ++i) {
+        long chunks = 0;
+        const int st = check_adamw(tensors[i], &chunks);
+        if (st != DG_OK) return st;
+        if (chunks > INT_MAX - total) return DG_ERR_UNSUPPORTED;   // the grid's limit
+        total += chunks;
+    }
+    return total;
 }
 
 }  // namespace
@@ -153,6 +191,78 @@ int dg_k_grouped_gemm_ragged_tn(const void* a, long lda, const void* b, long ldb
     p.nj = k;
     p.accumulate = accumulate;
     return launch_ragged(dg::kRaggedTN, dtype == DG_DTYPE_F16, d_dtype == DG_DTYPE_F32, p, stream);
+}
+
+long dg_adamw_plan_bytes(const dg_adamw_tensor* tensors, int count) {
+    const long chunks = count_chunks(tensors, count);
+    return chunks < 0 ? chunks : count * (long)sizeof(dg::AdamwEntry) + chunks * (long)sizeof(int);
+}
+
+int dg_adamw_plan(const dg_adamw_tensor* tensors, int count, void* table_host, long table_bytes) {
+    const long chunks = count_chunks(tensors, count);
+    if (chunks < 0) return (int)chunks;
+    const long bytes = count * (long)sizeof(dg::AdamwEntry) + chunks * (long)sizeof(int);
+    if (table_bytes != bytes || (bytes > 0 && !table_host)) return DG_ERR_INVALID_ARG;
+    // (the host table need not be aligned: entries are copied into it)
+    char* const entries = static_cast<char*>(table_host);
+    char* const tensor_of = entries + count * (long)sizeof(dg::AdamwEntry);
+    long at = 0;
+    for (int i = 0; i < count; ++i) {
+        const dg_adamw_tensor& t = tensors[i];
+        long own = 0;
+        (void)check_adamw(t, &own);
+        dg::AdamwEntry e{};
+        e.param = t.param;
+        e.grad = t.grad;
+        e.m = t.exp_avg;
+        e.v = t.exp_avg_sq;
+        e.m_scale = t.exp_avg_scale;
+        e.v_scale = t.exp_avg_sq_scale;
+        e.copy = t.copy;
+        e.numel = t.numel;
+        e.first_chunk = (int)at;
+        e.param_type = (uint8_t)t.param_dtype;
+        e.grad_type = (uint8_t)t.grad_dtype;
+        e.copy_type = (uint8_t)t.copy_dtype;
+        e.fp8 = t.state_format == DG_STATE_E4M3;
+        std::memcpy(entries + i * (long)sizeof(e), &e, sizeof(e));
+        for (long c = 0; c < own; ++c, ++at) std::memcpy(tensor_of + at * (long)sizeof(int), &i, sizeof(int));
+    }
+    return DG_OK;
+}
+
+int dg_adamw_step(const void* table, int count, long table_bytes, long step, double lr, double beta1, double beta2,
+                  double eps, double weight_decay, const float* grad_scale, void* stream) {
+    const long entries = count * (long)sizeof(dg::AdamwEntry);
+    if (count < 0 || table_bytes < entries || (table_bytes - entries) % (long)sizeof(int) || step < 1)
+        return DG_ERR_INVALID_ARG;
+    // (comparisons that a NaN fails)
+    if (!(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0) || !(eps >= 0.0) || !std::isfinite(eps) ||
+        !std::isfinite(lr) || !std::isfinite(weight_decay))
+        return DG_ERR_INVALID_ARG;
+    const long chunks = (table_bytes - entries) / (long)sizeof(int);
+    if (chunks > INT_MAX) return DG_ERR_INVALID_ARG;
+    if (chunks == 0) return DG_OK;
+    if (!table) return DG_ERR_INVALID_ARG;
+    if (!aligned(table, 8) || !aligned(grad_scale, 4)) return DG_ERR_MISALIGNED;
+    dg::AdamwParams p{};
+    p.entries = static_cast<const dg::AdamwEntry*>(table);
+    p.tensor_of = reinterpret_cast<const int*>(static_cast<const char*>(table) + entries);
+    p.grad_scale = grad_scale;
+    // the step's scalars in double, each rounded once to the fp32 the kernel works in
+    p.beta1 = (float)beta1;
+    p.one_minus_beta1 = (float)(1.0 - beta1);
+    p.beta2 = (float)beta2;
+    p.one_minus_beta2 = (float)(1.0 - beta2);
+    p.root2 = (float)(1.0 / std::sqrt(1.0 - std::pow(beta2, (double)step)));
+    p.eps = (float)eps;
+    p.decay = (float)(1.0 - lr * weight_decay);
+    p.size = (float)(lr / (1.0 - std::pow(beta1, (double)step)));
+    if (dg::launch_adamw(p, chunks, static_cast<hipStream_t>(stream)) != hipSuccess) {
+        (void)hipGetLastError();
+        return DG_ERR_HIP;
+    }
+    return DG_OK;
 }
 
 }  // extern "C"

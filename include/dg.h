@@ -239,6 +239,60 @@ int dg_k_grouped_gemm_ragged_tn(const void* a, long lda, const void* b, long ldb
                                 const int* offsets, int m_total, int n, int k, int num_groups,
                                 int dtype, int d_dtype, int accumulate, void* stream);
 
+/* ---- Training operators: an AdamW step over many tensors at once ----
+ *
+ *   g = grad * grad_scale;  m = beta1 m + (1 - beta1) g;  v = beta2 v + (1 - beta2) g^2
+ *   p = p (1 - lr weight_decay) - lr / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+ *
+ * in fp32, one launch for all tensors of a plan.  A tensor is numel consecutive elements:
+ *   param       fp32 or BF16, updated in place (BF16 is rounded to nearest even)
+ *   grad        fp32, BF16 or FP16, read only
+ *   exp_avg, exp_avg_sq   m and v: fp32 (DG_STATE_F32), or E4M3 codes (DG_STATE_E4M3)
+ *   exp_avg_scale, exp_avg_sq_scale   [ceil(numel / 128)] fp32, 8-bit states only
+ *   copy        optional BF16 or FP16 copy of the updated param, for the products to read
+ * 8-bit states: elements 128 b .. 128 b + 127 share scale[b] = fp32(amax / 448) (1 if amax is
+ * 0) and the codes are E4M3 round-to-nearest-even of fp32(x / scale), as the casts' are.  A
+ * code c of exp_avg stands for c * scale; one of exp_avg_sq holds the root, it stands for
+ * (c * scale)^2, and a root that is not zero never gets code zero.  All-zero codes with any
+ * finite scales are a fresh state.  Every operation is rounded once, so codes and
+ * scales are a deterministic function of the inputs.  A gradient that is NaN or infinite
+ * spoils its element for good, and with 8-bit states its block: test for it first. */
+enum { DG_STATE_F32 = 0, DG_STATE_E4M3 = 1 };
+
+typedef struct dg_adamw_tensor {
+    void* param;
+    const void* grad;
+    void* exp_avg;
+    void* exp_avg_sq;
+    float* exp_avg_scale;      /* NULL with DG_STATE_F32 */
+    float* exp_avg_sq_scale;
+    void* copy;                /* or NULL */
+    long numel;
+    int param_dtype;           /* DG_DTYPE_F32, DG_DTYPE_BF16 */
+    int grad_dtype;            /* DG_DTYPE_F32, DG_DTYPE_BF16, DG_DTYPE_F16 */
+    int copy_dtype;            /* DG_DTYPE_BF16, DG_DTYPE_F16 (where copy is given) */
+    int state_format;          /* DG_STATE_* */
+} dg_adamw_tensor;
+
+/* A plan is a table in device memory that names the tensors.  dg_adamw_plan_bytes gives its
+ * size (or a negative status), dg_adamw_plan writes it to host memory of exactly that
+ * size; the caller copies it to the device (8-byte aligned) and keeps it while the tensors
+ * stay where they are.  Host only; `tensors` is a host array of device pointers, all 16-byte
+ * aligned (codes 8, scales 4; else DG_ERR_MISALIGNED).  Null pointers, unknown types and
+ * negative sizes give DG_ERR_INVALID_ARG, more than 2^31 - 1 chunks of 2048 elements
+ * DG_ERR_UNSUPPORTED.  Tensors of no elements are allowed; no two may overlap. */
+long dg_adamw_plan_bytes(const dg_adamw_tensor* tensors, int count);
+int dg_adamw_plan(const dg_adamw_tensor* tensors, int count, void* table_host, long table_bytes);
+
+/* One step t = `step` (from 1) of the plan whose table, of `count` tensors and table_bytes
+ * bytes, lies at `table` on the device.  grad_scale: one fp32 on the device that multiplies every
+ * gradient (a clipping coefficient, an inverse loss scale), or NULL.  The scalars are
+ * computed in double and rounded to fp32.  step < 1, betas outside [0, 1), a negative eps or
+ * scalars that are not finite give DG_ERR_INVALID_ARG.  Asynchronous on `stream`; a captured
+ * step keeps its scalars. */
+int dg_adamw_step(const void* table, int count, long table_bytes, long step, double lr, double beta1,
+                  double beta2, double eps, double weight_decay, const float* grad_scale, void* stream);
+
 /* Leading dimension (in floats) that an MN-major sA of `rows` rows needs: rows rounded
  * up to a multiple of 4, so that every K block's scales start 16-byte aligned (the
  * README's utility get_tma_aligned_size, for the GEMMs here).  rows < 0 gives
