@@ -96,6 +96,10 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.dg_m_grouped_gemm_ragged_nn.restype = I
     lib.dg_k_grouped_gemm_ragged_tn.argtypes = [P, L, P, L, P, P, I, I, I, I, I, I, I, P]
     lib.dg_k_grouped_gemm_ragged_tn.restype = I
+    lib.dg_set_ragged_tile.argtypes = [I, I]
+    lib.dg_set_ragged_tile.restype = I
+    lib.dg_ragged_tile_info.argtypes = [I, P]
+    lib.dg_ragged_tile_info.restype = I
     D = ctypes.c_double
     lib.dg_adamw_plan_bytes.argtypes = [P, I]
     lib.dg_adamw_plan_bytes.restype = L
@@ -635,6 +639,19 @@ def dg_set_kernel_config(config_id: int) -> None:
     _check(load_library().dg_set_kernel_config(int(config_id)), "dg_set_kernel_config")
 
 
+def dg_set_ragged_tile(block_m: int, block_n: int) -> None:
+    """Pin the tile of the calling thread's ragged products (0, 0: plan again)."""
+    _check(load_library().dg_set_ragged_tile(int(block_m), int(block_n)), "dg_set_ragged_tile")
+
+
+def dg_ragged_tile_info() -> list:
+    """The tiles (block_m, block_n) that ragged products are compiled for."""
+    out, res = (ctypes.c_int * 2)(), []
+    while load_library().dg_ragged_tile_info(len(res), out) == DG_OK:
+        res.append(tuple(out))
+    return res
+
+
 def dg_kernel_config_info() -> list:
     """All compiled kernel configurations as dicts (id, layout, block_m, block_n, waves,
     all_formats: whether E5M2 operands run in it, shape_specialised: whether it has
@@ -681,7 +698,7 @@ __all__ = [
     "dg_check_contiguous_layout", "dg_plan_tiles",
     "dg_m_grouped_gemm_ragged_nt", "dg_m_grouped_gemm_ragged_nn", "dg_k_grouped_gemm_ragged_tn",
     "AdamWPlan", "DG_STATE_F32", "DG_STATE_E4M3", "dg_adamw_plan_bytes", "dg_adamw_plan", "dg_adamw_step",
-    "dg_set_kernel_config", "dg_kernel_config_info", "dg_describe_launch",
+    "dg_set_kernel_config", "dg_kernel_config_info", "dg_describe_launch", "dg_set_ragged_tile", "dg_ragged_tile_info",
     "gemm_fp8_fp8_bf16_nt", "m_grouped_gemm_fp8_fp8_bf16_nt_contiguous", "m_grouped_gemm_fp8_fp8_bf16_nt_masked",
     "set_num_sms", "get_num_sms", "get_m_alignment_for_contiguous_layout", "get_tma_aligned_size",
     "get_col_major_tma_aligned_tensor",

@@ -30,9 +30,9 @@ __device__ __forceinline__ void unroll(F&& f) {
 }
 
 // Raw buffer descriptor over `bytes` bytes from `base`: a lane whose offset lies at or
-// past the end reads zeros and touches no memory.  The callers keep every offset that is
-// meant to be inside below 2^31, so kOutside is outside of each.
-constexpr uint32_t kOutside = 0xFFFFFF00u;
+// past the end reads zeros and touches no memory.  No descriptor reaches 2^31 bytes and the
+// callers keep every offset below that, so kOutside, plus any of them, is outside of each.
+constexpr uint32_t kOutside = 0x80000000u;
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_over(const void* base, long bytes) {
     const unsigned n = bytes <= 0 ? 0u : (bytes >= 0x7FFFFFFFl ? 0x7FFFFFFFu : (unsigned)bytes);
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, (int)n, 0x00020000);

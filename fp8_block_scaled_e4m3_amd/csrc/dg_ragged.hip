@@ -63,11 +63,25 @@ __device__ __forceinline__ void unpack2(uint32_t w, float& x, float& y) {
 }
 
 // Swizzles (see the head of the file).  Contiguous operand: 16-byte chunk of a 128-byte
-// row; eight and sixteen consecutive rows read at one chunk fall into distinct banks.
-__device__ __forceinline__ int swz_row(int row) { return (row & 7) ^ ((row >> 3) & 1); }
+// row.  A 16-byte read takes a wave's lanes sixteen at a time, and not in order: four runs of
+// four that pair rows 0-3 and 12-15 of one chunk with rows 4-11 of its neighbour.  This one
+// keeps those sixteen, as well as any sixteen lanes in order, in distinct banks (an earlier one
+// that did only the latter doubled the reads' time: 4 conflict cycles in 8).
+__device__ __forceinline__ int swz_row(int row) { return (row >> 1) & 7; }
 // Strided operand: 32-byte unit of a row of one c.  Half a wave's transposing read covers
 // four consecutive c in each of two groups eight apart: eight rows, eight distinct units.
 __device__ __forceinline__ int swz_c(int c) { return (c & 3) | (((c >> 3) & 1) << 2); }
+
+// Tile r of a group of ni x nj tiles: bands of kBand row tiles, down a band's column before
+// the next column.  The 32 tiles that an XCD works on at a time are then a block of 8 x 4,
+// whose operands its L2 fetches once.
+constexpr int kBand = 8;
+__device__ __forceinline__ void band_order(long r, int ni, int nj, int& ti, int& tj) {
+    const int band = (int)(r / ((long)kBand * nj));
+    const int rest = (int)(r - (long)band * kBand * nj), height = min(kBand, ni - band * kBand);
+    ti = band * kBand + rest % height;
+    tj = rest / height;
+}
 
 template <typename T, int OP, int BM, int BN, int WM, int WN, bool OUT32>
 __global__ void __launch_bounds__(WM * WN * 64)
@@ -142,14 +156,26 @@ ragged_gemm_kernel(const RaggedParams p) {
         total = (long)s_tiles[G] * p.tiles_j;
     }
 
-    // ---- a lane's place in its copies ----
-    // contiguous: slot = 8 rows of 128 bytes; strided: slot = RPS rows of B elements
+    // ---- a lane's place in its copies.  A copy is 1 KiB of a stage: 8 rows of 128 bytes
+    // (contiguous) or RPS rows of BM or BN elements (strided).  A wave's copies are NW slots
+    // apart, a multiple of 16 rows, so that they share the lane's swizzled chunk and differ
+    // by a whole number of rows. ----
     constexpr int P_RPS = PS ? 512 / BM : 8, Q_RPS = QS ? 512 / BN : 8;
-    auto slot_row = [&](int slot, int rps) DG_DEV_INLINE { return slot * rps + lane / (64 / rps); };
-    auto slot_chunk = [&](int row, int rps, bool strided) DG_DEV_INLINE {
-        const int c = lane % (64 / rps);
-        return strided ? c ^ (swz_c(row) * 2) : c ^ swz_row(row);
-    };
+    static_assert(NW * P_RPS % 16 == 0 && NW * Q_RPS % 16 == 0, "the swizzles' period");
+    const int p_row = wave * P_RPS + lane / (64 / P_RPS), q_row = wave * Q_RPS + lane / (64 / Q_RPS);
+    const int p_chunk = (lane % (64 / P_RPS)) ^ (PS ? swz_c(p_row) * 2 : swz_row(p_row));
+    const int q_chunk = (lane % (64 / Q_RPS)) ^ (QS ? swz_c(q_row) * 2 : swz_row(q_row));
+    const uint32_t p_lane = (uint32_t)(p_row * p.ldp + p_chunk * 8) * 2u, q_lane = (uint32_t)(q_row * p.ldq + q_chunk * 8) * 2u;
+    const uint32_t p_next = (uint32_t)(NW * P_RPS * p.ldp) * 2u, q_next = (uint32_t)(NW * Q_RPS * p.ldq) * 2u;
+
+    // ---- a lane's place in its fragments: byte offset in an operand's part of a stage of
+    // sub-tile 0 of half 0; strided operands add (xor) the sub-tile's 32-byte unit to it, and
+    // constants lead to the other sub-tiles and halves ----
+    const int tr_c = lgrp * 8 + (l16 >> 2), tr_swz = swz_c(tr_c);
+    const int p_frag = PS ? tr_c * BM * 2 + ((wm * (WTM / 16)) ^ tr_swz) * 32 + (l16 & 3) * 8
+                          : (wm * WTM + l16) * 128 + (lgrp ^ swz_row(l16)) * 16;
+    const int q_frag = QS ? tr_c * BN * 2 + ((wn * (WTN / 16)) ^ tr_swz) * 32 + (l16 & 3) * 8
+                          : (wn * WTN + l16) * 128 + (lgrp ^ swz_row(l16)) * 16;
 
     for (long L0 = 0; L0 < total; L0 += gridDim.x) {
         const int P = gridDim.x, w = blockIdx.x;
@@ -162,9 +188,10 @@ ragged_gemm_kernel(const RaggedParams p) {
         if constexpr (OP == kRaggedTN) {
             const int per = p.tiles_i * p.tiles_j;
             g = (int)(L / per);
-            const int r = (int)(L - (long)g * per);
-            i0 = r / p.tiles_j * BM;
-            j0 = r % p.tiles_j * BN;
+            int ti, tj;
+            band_order((int)(L - (long)g * per), p.tiles_i, p.tiles_j, ti, tj);
+            i0 = ti * BM;
+            j0 = tj * BN;
         } else {
             const int q = (int)(L / p.tiles_j);
             int lo = 0, hi = G;        // the last g with s_tiles[g] <= q
@@ -174,9 +201,10 @@ ragged_gemm_kernel(const RaggedParams p) {
             }
             g = lo;
             const int rt = s_tiles[g + 1] - s_tiles[g];
-            const long r = L - (long)s_tiles[g] * p.tiles_j;
-            j0 = (int)(r / rt) * BN;
-            i0 = (int)(r % rt) * BM;
+            int ti, tj;
+            band_order(L - (long)s_tiles[g] * p.tiles_j, rt, p.tiles_j, ti, tj);
+            i0 = ti * BM;
+            j0 = tj * BN;
         }
         g = __builtin_amdgcn_readfirstlane(g);
         i0 = __builtin_amdgcn_readfirstlane(i0);
@@ -192,19 +220,8 @@ ragged_gemm_kernel(const RaggedParams p) {
         const uint16_t* qb = p.q + (OP == kRaggedTN ? (long)seg0 * p.ldq + j0
                                     : QS ? (long)g * p.q_gstride + j0
                                          : (long)g * p.q_gstride + (long)j0 * p.ldq);
-        uint32_t p_off[P_PER], q_off[Q_PER];
-#pragma unroll
-        for (int i = 0; i < P_PER; ++i) {
-            const int row = slot_row(wave + i * NW, P_RPS), ch = slot_chunk(row, P_RPS, PS);
-            p_off[i] = (uint32_t)(row * p.ldp + ch * 8) * 2u;
-            if (PS && i0 + ch * 8 >= p.ni) p_off[i] = kOutside;
-        }
-#pragma unroll
-        for (int i = 0; i < Q_PER; ++i) {
-            const int row = slot_row(wave + i * NW, Q_RPS), ch = slot_chunk(row, Q_RPS, QS);
-            q_off[i] = (uint32_t)(row * p.ldq + ch * 8) * 2u;
-            if (QS && j0 + ch * 8 >= p.nj) q_off[i] = kOutside;
-        }
+        const uint32_t p_off = PS && i0 + p_chunk * 8 >= p.ni ? kOutside : p_lane;
+        const uint32_t q_off = QS && j0 + q_chunk * 8 >= p.nj ? kOutside : q_lane;
         // contiguous operands: one descriptor for the tile, the step in the scalar offset, the
         // contraction's end by lane; strided ones: a descriptor per step, over the rows left
         const __amdgpu_buffer_rsrc_t p_rs = buffer_over(pb, (long)min(ni - i0, BM) * p.ldp * 2);
@@ -214,36 +231,29 @@ ragged_gemm_kernel(const RaggedParams p) {
             const bool tail = left < kStep;
             const __amdgpu_buffer_rsrc_t pr = PS ? buffer_over(pb + (long)c0 * p.ldp, (long)min(left, kStep) * p.ldp * 2) : p_rs;
             const __amdgpu_buffer_rsrc_t qr = QS ? buffer_over(qb + (long)c0 * p.ldq, (long)min(left, kStep) * p.ldq * 2) : q_rs;
+            const uint32_t po = !PS && tail && p_chunk * 8 >= left ? kOutside : p_off;
+            const uint32_t qo = !QS && tail && q_chunk * 8 >= left ? kOutside : q_off;
 #pragma unroll
-            for (int i = 0; i < P_PER; ++i) {
-                const int slot = wave + i * NW;
-                uint32_t off = p_off[i];
-                if (!PS && tail && slot_chunk(slot_row(slot, P_RPS), P_RPS, PS) * 8 >= left) off = kOutside;
-                copy_to_lds16(pr, (lds_void*)(st + slot * 1024), off, PS ? 0u : (uint32_t)c0 * 2u);
-            }
+            for (int i = 0; i < P_PER; ++i)
+                copy_to_lds16(pr, (lds_void*)(st + (wave + i * NW) * 1024), po + i * p_next, PS ? 0u : (uint32_t)c0 * 2u);
 #pragma unroll
-            for (int i = 0; i < Q_PER; ++i) {
-                const int slot = wave + i * NW;
-                uint32_t off = q_off[i];
-                if (!QS && tail && slot_chunk(slot_row(slot, Q_RPS), Q_RPS, QS) * 8 >= left) off = kOutside;
-                copy_to_lds16(qr, (lds_void*)(st + P_BYTES + slot * 1024), off, QS ? 0u : (uint32_t)c0 * 2u);
-            }
+            for (int i = 0; i < Q_PER; ++i)
+                copy_to_lds16(qr, (lds_void*)(st + P_BYTES + (wave + i * NW) * 1024), qo + i * q_next, QS ? 0u : (uint32_t)c0 * 2u);
         };
 
-        // fragment f (16 of i or j, from x0) of half h (32 c) of an operand at LDS base `b`
-        auto frag_row = [&](const uint8_t* b, int x0, int h) DG_DEV_INLINE -> v4i {
+        // Fragment of sub-tile f, half h.  The lane's offset is hidden from the compiler at each
+        // use, so that it computes the few addresses it needs (one xor or a constant offset
+        // each) instead of keeping one register for every fragment of every stage.
+        auto frag_row = [&](const uint8_t* b, int at, int f, int h) DG_DEV_INLINE -> v4i {
             typedef __attribute__((address_space(3))) const v4i lds_v4i;
-            const int row = x0 + l16;
-            return *(lds_v4i*)((const lds_u8*)b + row * 128 + (((h * 4 + lgrp) ^ swz_row(row)) * 16));
+            return *(lds_v4i*)((const lds_u8*)b + ((at ^ (h * 64)) + f * 2048));
         };
-        auto frag_tr = [&](const uint8_t* b, int x0, int h, int width) DG_DEV_INLINE -> v4i {
+        auto frag_tr = [&](const uint8_t* b, int at, int f, int h, int width) DG_DEV_INLINE -> v4i {
             typedef short v4s __attribute__((ext_vector_type(4)));
             typedef __attribute__((address_space(3))) v4s lds_v4s;
-            const int c = h * 32 + lgrp * 8 + (l16 >> 2);
-            const int unit = (x0 / 16) ^ swz_c(c);
-            lds_u8* at = (lds_u8*)b + c * width * 2 + unit * 32 + (l16 & 3) * 8;
-            const v2i lo = __builtin_bit_cast(v2i, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)at));
-            const v2i hi = __builtin_bit_cast(v2i, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(at + 4 * width * 2)));
+            lds_u8* a = (lds_u8*)b + ((at ^ (f * 32)) + h * 32 * width * 2);
+            const v2i lo = __builtin_bit_cast(v2i, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)a));
+            const v2i hi = __builtin_bit_cast(v2i, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(a + 4 * width * 2)));
             return v4i{lo.x, lo.y, hi.x, hi.y};
         };
 
@@ -253,45 +263,60 @@ ragged_gemm_kernel(const RaggedParams p) {
 #pragma unroll
             for (int fn = 0; fn < FN; ++fn) acc[fm][fn] = v4f{0.f, 0.f, 0.f, 0.f};
 
-        auto compute = [&](const uint8_t* st) DG_DEV_INLINE {
+        // fragments of half h of a step: one set is multiplied while the other is read
+        v4i pf[2][FM], qf[2][FN];
+        auto read_half = [&](const uint8_t* st, auto half) DG_DEV_INLINE {
+            constexpr int h = decltype(half)::value;
+            int pa = p_frag, qa = q_frag;
+            asm volatile("" : "+v"(pa), "+v"(qa));
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                v4i pf[FM], qf[FN];
+            for (int fn = 0; fn < FN; ++fn) qf[h][fn] = QS ? frag_tr(st + P_BYTES, qa, fn, h, BN) : frag_row(st + P_BYTES, qa, fn, h);
 #pragma unroll
-                for (int fm = 0; fm < FM; ++fm) {
-                    const int x0 = wm * WTM + fm * 16;
-                    pf[fm] = PS ? frag_tr(st, x0, h, BM) : frag_row(st, x0, h);
-                }
+            for (int fm = 0; fm < FM; ++fm) pf[h][fm] = PS ? frag_tr(st, pa, fm, h, BM) : frag_row(st, pa, fm, h);
+        };
+        auto multiply_half = [&](auto half) DG_DEV_INLINE {
+            constexpr int h = decltype(half)::value;
 #pragma unroll
-                for (int fn = 0; fn < FN; ++fn) {
-                    const int x0 = wn * WTN + fn * 16;
-                    qf[fn] = QS ? frag_tr(st + P_BYTES, x0, h, BN) : frag_row(st + P_BYTES, x0, h);
-                }
+            for (int fm = 0; fm < FM; ++fm)
 #pragma unroll
-                for (int fn = 0; fn < FN; ++fn)
-#pragma unroll
-                    for (int fm = 0; fm < FM; ++fm) acc[fm][fn] = T::mfma(qf[fn], pf[fm], acc[fm][fn]);
-            }
+                for (int fn = 0; fn < FN; ++fn) acc[fm][fn] = T::mfma(qf[h][fn], pf[h][fm], acc[fm][fn]);
         };
 
-        // ---- contraction: copies of step s + 1 fly while step s is computed ----
+        // ---- contraction.  The one barrier of a step sits between its halves: by then every
+        // wave holds the second half's fragments, so the stage is free for the copies of the
+        // step after next, and every wave's copies of the next step have landed, so its
+        // first half is read while this step's second half is multiplied. ----
         if (steps > 0) {
+            constexpr std::integral_constant<int, 0> first{};
+            constexpr std::integral_constant<int, 1> second{};
+            constexpr int NCOPY = P_PER + Q_PER;
             issue(smem0, 0);
+            if (steps > 1) {
+                issue(smem1, 1);
+                wait_vmem<NCOPY>();
+            } else {
+                wait_vmem<0>();
+            }
+            barrier_only();
+            read_half(smem0, first);
             auto step = [&](int s, uint8_t* cur, uint8_t* next) DG_DEV_INLINE {
-                // (the wave's own copies of step s, then everyone's; and everyone is done
-                // reading the stage that the next copies fill)
+                read_half(cur, second);
+                __builtin_amdgcn_sched_barrier(0);
+                multiply_half(first);
+                __builtin_amdgcn_sched_barrier(0);
                 wait_vmem<0>();
                 wait_lds();
                 barrier_only();
-                if (s + 1 < steps) issue(next, s + 1);
-                compute(cur);
+                if (s + 2 < steps) issue(cur, s + 2);
+                if (s + 1 < steps) read_half(next, first);
+                __builtin_amdgcn_sched_barrier(0);
+                multiply_half(second);
+                __builtin_amdgcn_sched_barrier(0);
             };
             for (int s = 0; s < steps; s += 2) {
                 step(s, smem0, smem1);
                 if (s + 1 < steps) step(s + 1, smem1, smem0);
             }
-            wait_lds();
-            barrier_only();      // the stages are free for the next tile
         }
 
         // ---- epilogue: lane l16 holds row l16 of a sub-tile, columns 4 lgrp .. + 3 ----
@@ -363,14 +388,20 @@ hipError_t occupancy_ragged(int* blocks) {
                                                         WM * WN * 64, 0);
 }
 
-#define DG_RAGGED(T, HALF, OP, BM, BN, WM, WN, OUT32)                                           \
-    {OP, HALF, OUT32, BM, BN, &launch_ragged<T, OP, BM, BN, WM, WN, OUT32>,                     \
-     &occupancy_ragged<T, OP, BM, BN, WM, WN, OUT32>}
-#define DG_RAGGED_TYPE(T, HALF)                                \
-    DG_RAGGED(T, HALF, kRaggedNT, 128, 128, 2, 2, false),      \
-    DG_RAGGED(T, HALF, kRaggedNN, 128, 128, 2, 2, false),      \
-    DG_RAGGED(T, HALF, kRaggedTN, 128, 128, 2, 2, false),      \
-    DG_RAGGED(T, HALF, kRaggedTN, 128, 128, 2, 2, true)
+// Relative times: 1024 256x256 tiles' worth of products take 4 (one workgroup a CU), with
+// 128x128 tiles (two a CU) 1/0.85 of it, from the forward pass of 32768 x 4096 x 7168 in
+// eight groups: 1647 us and 1929 us.  Few tiles: 64 x 4096 x 7168 in 16 groups 193 us and 156 us.
+#define DG_RAGGED_256(T, HALF, OP, OUT32)                                                  \
+    {OP, HALF, OUT32, 256, 256, 4.0, 4.0, &launch_ragged<T, OP, 256, 256, 2, 4, OUT32>,    \
+     &occupancy_ragged<T, OP, 256, 256, 2, 4, OUT32>}
+#define DG_RAGGED_128(T, HALF, OP, OUT32)                                                  \
+    {OP, HALF, OUT32, 128, 128, 2.35, 1.4, &launch_ragged<T, OP, 128, 128, 2, 2, OUT32>,   \
+     &occupancy_ragged<T, OP, 128, 128, 2, 2, OUT32>}
+#define DG_RAGGED_TYPE(T, HALF)                                                            \
+    DG_RAGGED_256(T, HALF, kRaggedNT, false), DG_RAGGED_128(T, HALF, kRaggedNT, false),    \
+    DG_RAGGED_256(T, HALF, kRaggedNN, false), DG_RAGGED_128(T, HALF, kRaggedNN, false),    \
+    DG_RAGGED_256(T, HALF, kRaggedTN, false), DG_RAGGED_128(T, HALF, kRaggedTN, false),    \
+    DG_RAGGED_256(T, HALF, kRaggedTN, true), DG_RAGGED_128(T, HALF, kRaggedTN, true)
 
 const RaggedConfig kConfigs[] = {DG_RAGGED_TYPE(Bf16, 0), DG_RAGGED_TYPE(F16, 1)};
 

@@ -32,6 +32,9 @@ struct RaggedConfig {
     int half;                // 0: BF16 operands, 1: FP16
     int out_f32;             // D in fp32 (else in the operands' type)
     int bm, bn;              // tile of D
+    // relative time per step of c: of a round of tiles that fills the CUs, and of one
+    // tile with a CU to itself
+    double round_time, alone_time;
     hipError_t (*launch)(const RaggedParams&, int grid, hipStream_t);
     hipError_t (*occupancy)(int* blocks_per_cu);
 };

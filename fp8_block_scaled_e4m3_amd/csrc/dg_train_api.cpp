@@ -12,12 +12,16 @@
 #include <cstring>
 
 #include "../../include/dg.h"
+#include "../../include/dg_tuning.h"
 #include "dg_train.h"
 
 namespace {
 
 constexpr int kMaxConfigs = 64;
 constexpr long kMaxLd = 1l << 22;      // a tile's copies use 31-bit offsets: 256 rows of ld elements
+
+// dg_set_ragged_tile: 0 plans.  Per thread, like dg_set_kernel_config.
+thread_local int g_pinned_bm = 0, g_pinned_bn = 0;
 
 bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
 
@@ -37,6 +41,16 @@ int blocks_per_cu(const dg::RaggedConfig* c, int index) {
     return v;
 }
 
+// Expected tiles of D, for the choice of a tile: a filled group wastes half a row tile on
+// average, and has one at least.
+double tiles_expected(int op, const dg::RaggedParams& p, int bm, int bn) {
+    const double columns = (double)ceil_div(p.nj, bn);
+    if (op == dg::kRaggedTN) return (double)p.groups * ceil_div(p.ni, bm) * columns;
+    const double filled = p.groups < p.rows ? p.groups : p.rows;
+    const double split = (double)p.rows / bm + 0.5 * filled;
+    return (split > filled ? split : filled) * columns;
+}
+
 // Upper bound of the tiles of D: the rows' exact split over the groups is on the device.
 long tiles_bound(int op, const dg::RaggedParams& p, int bm, int bn) {
     if (op == dg::kRaggedTN) return (long)p.groups * ceil_div(p.ni, bm) * ceil_div(p.nj, bn);
@@ -49,9 +63,24 @@ int launch_ragged(int op, int half, int out_f32, dg::RaggedParams& p, void* stre
     const dg::RaggedConfig* cfgs = dg::ragged_configs(&count);
     const int units = dg_get_num_cus();
     if (units < 0) return DG_ERR_HIP;
+    // the tile whose rounds over the CUs take least time (RaggedConfig::round_time)
     int best = -1;
-    for (int i = 0; i < count && i < kMaxConfigs; ++i)
-        if (cfgs[i].op == op && cfgs[i].half == half && cfgs[i].out_f32 == out_f32) best = i;
+    double best_time = 0.0;
+    for (int i = 0; i < count && i < kMaxConfigs; ++i) {
+        const dg::RaggedConfig& c = cfgs[i];
+        if (c.op != op || c.half != half || c.out_f32 != out_f32) continue;
+        if (c.bm == g_pinned_bm && c.bn == g_pinned_bn) {
+            best = i;
+            break;
+        }
+        const double tiles = tiles_expected(op, p, c.bm, c.bn);
+        const double time = tiles <= units ? c.alone_time
+                                           : std::ceil(tiles / ((double)units * blocks_per_cu(&c, i))) * c.round_time;
+        if (best < 0 || time < best_time) {
+            best = i;
+            best_time = time;
+        }
+    }
     if (best < 0) return DG_ERR_UNSUPPORTED;
     const dg::RaggedConfig& c = cfgs[best];
     p.tiles_i = (int)ceil_div(p.ni, c.bm);
@@ -119,6 +148,30 @@ long count_chunks(const dg_adamw_tensor* tensors, int count) {
 }  // namespace
 
 extern "C" {
+
+int dg_ragged_tile_info(int index, int* out) {
+    int count = 0;
+    const dg::RaggedConfig* cfgs = dg::ragged_configs(&count);
+    if (!out || index < 0) return DG_ERR_INVALID_ARG;
+    for (int i = 0; i < count; ++i) {
+        bool seen = false;
+        for (int j = 0; j < i; ++j) seen |= cfgs[j].bm == cfgs[i].bm && cfgs[j].bn == cfgs[i].bn;
+        if (seen || index-- != 0) continue;
+        out[0] = cfgs[i].bm;
+        out[1] = cfgs[i].bn;
+        return DG_OK;
+    }
+    return DG_ERR_INVALID_ARG;
+}
+
+int dg_set_ragged_tile(int block_m, int block_n) {
+    int tile[2] = {0, 0};
+    for (int i = 0; tile[0] != block_m || tile[1] != block_n; ++i)
+        if (dg_ragged_tile_info(i, tile) != DG_OK) return DG_ERR_INVALID_ARG;
+    g_pinned_bm = block_m;
+    g_pinned_bn = block_n;
+    return DG_OK;
+}
 
 int dg_m_grouped_gemm_ragged_nt(const void* a, long lda, const void* b, void* d, long ldd, const int* offsets,
                                 int m_total, int n, int k, int num_groups, int dtype, void* stream) {

@@ -7,6 +7,7 @@ products per step, so the number of terms bounds its additions).  Rounding to D'
 the element lies between the roundings of exact - E and exact + E."""
 import numpy as np
 import pytest
+import torch  # noqa: F401  (before the library is loaded, at collection: both then share torch's HIP runtime)
 
 import fp8_block_scaled_e4m3_amd as dg
 from tests.gpu_support import require_gpu, say
@@ -20,6 +21,14 @@ SENTINEL = -77.0
 def gpu():
     require_gpu()
     dg.load_library()
+
+
+@pytest.fixture(autouse=True, params=[(0, 0)] + dg.dg_ragged_tile_info(), ids=lambda t: f"{t[0]}x{t[1]}")
+def tile(request):
+    """Every test runs as planned and with each compiled tile."""
+    dg.dg_set_ragged_tile(*request.param)
+    yield request.param
+    dg.dg_set_ragged_tile(0, 0)
 
 
 def types():

@@ -68,6 +68,15 @@ def test_weight_gradient_refuses(lib, change, status):
     assert lib.dg_k_grouped_gemm_ragged_tn(*args.values()) == status
 
 
+def test_ragged_tile_hooks(lib):
+    tiles = dg.dg_ragged_tile_info()
+    assert (128, 128) in tiles and (256, 256) in tiles and len(set(tiles)) == len(tiles)
+    for t in tiles + [(0, 0)]:
+        dg.dg_set_ragged_tile(*t)
+    assert lib.dg_set_ragged_tile(17, 32) == INVALID and lib.dg_ragged_tile_info(0, None) == INVALID
+    assert lib.dg_ragged_tile_info(-1, (ctypes.c_int * 2)()) == INVALID
+
+
 def tensor(**change):
     t = dg._AdamwTensor(param=0x1000, grad=0x2000, exp_avg=0x3000, exp_avg_sq=0x4000, numel=5000, param_dtype=F32,
                         grad_dtype=BF16, copy_dtype=0, state_format=dg.DG_STATE_F32)
