@@ -224,21 +224,25 @@ ragged_gemm_kernel(const RaggedParams p) {
         const uint32_t q_off = QS && j0 + q_chunk * 8 >= p.nj ? kOutside : q_lane;
         // contiguous operands: one descriptor for the tile, the step in the scalar offset, the
         // contraction's end by lane; strided ones: a descriptor per step, over the rows left
-        const __amdgpu_buffer_rsrc_t p_rs = buffer_over(pb, (long)min(ni - i0, BM) * p.ldp * 2);
-        const __amdgpu_buffer_rsrc_t q_rs = buffer_over(qb, (long)min(p.nj - j0, BN) * p.ldq * 2);
-        auto issue = [&](uint8_t* st, int s) DG_DEV_INLINE {
+        const long p_bytes = (long)min(ni - i0, BM) * p.ldp * 2, q_bytes = (long)min(p.nj - j0, BN) * p.ldq * 2;
+        struct Copies { __amdgpu_buffer_rsrc_t pr, qr; uint32_t po, qo, soff; };
+        auto copies_of = [&](int s) DG_DEV_INLINE -> Copies {
             const int c0 = s * kStep, left = nc - c0;
-            const bool tail = left < kStep;
-            const __amdgpu_buffer_rsrc_t pr = PS ? buffer_over(pb + (long)c0 * p.ldp, (long)min(left, kStep) * p.ldp * 2) : p_rs;
-            const __amdgpu_buffer_rsrc_t qr = QS ? buffer_over(qb + (long)c0 * p.ldq, (long)min(left, kStep) * p.ldq * 2) : q_rs;
-            const uint32_t po = !PS && tail && p_chunk * 8 >= left ? kOutside : p_off;
-            const uint32_t qo = !QS && tail && q_chunk * 8 >= left ? kOutside : q_off;
-#pragma unroll
-            for (int i = 0; i < P_PER; ++i)
-                copy_to_lds16(pr, (lds_void*)(st + (wave + i * NW) * 1024), po + i * p_next, PS ? 0u : (uint32_t)c0 * 2u);
-#pragma unroll
-            for (int i = 0; i < Q_PER; ++i)
-                copy_to_lds16(qr, (lds_void*)(st + P_BYTES + (wave + i * NW) * 1024), qo + i * q_next, QS ? 0u : (uint32_t)c0 * 2u);
+            const bool some = left > 0, tail = left < kStep;
+            return Copies{PS ? buffer_over(pb + (long)c0 * p.ldp, (long)min(left, kStep) * p.ldp * 2)
+                             : buffer_over(pb, some ? p_bytes : 0),
+                          QS ? buffer_over(qb + (long)c0 * p.ldq, (long)min(left, kStep) * p.ldq * 2)
+                             : buffer_over(qb, some ? q_bytes : 0),
+                          !PS && tail && p_chunk * 8 >= left ? kOutside : p_off,
+                          !QS && tail && q_chunk * 8 >= left ? kOutside : q_off, some ? (uint32_t)c0 * 2u : 0u};
+        };
+        auto copy_one = [&](uint8_t* st, const Copies& c, int i) DG_DEV_INLINE {
+            if (i < P_PER) {
+                copy_to_lds16(c.pr, (lds_void*)(st + (wave + i * NW) * 1024), c.po + i * p_next, PS ? 0u : c.soff);
+            } else {
+                i -= P_PER;
+                copy_to_lds16(c.qr, (lds_void*)(st + P_BYTES + (wave + i * NW) * 1024), c.qo + i * q_next, QS ? 0u : c.soff);
+            }
         };
 
         // Fragment of sub-tile f, half h.  The lane's offset is hidden from the compiler at each
@@ -265,21 +269,35 @@ ragged_gemm_kernel(const RaggedParams p) {
 
         // fragments of half h of a step: one set is multiplied while the other is read
         v4i pf[2][FM], qf[2][FN];
-        auto read_half = [&](const uint8_t* st, auto half) DG_DEV_INLINE {
-            constexpr int h = decltype(half)::value;
+        constexpr int NREAD = FM + FN, NCOPY = P_PER + Q_PER;
+        // read i of a half, in the order in which the products need them
+        auto read_one = [&](const uint8_t* st, int pa, int qa, int h, int i) DG_DEV_INLINE {
+            if (i < FN) qf[h][i] = QS ? frag_tr(st + P_BYTES, qa, i, h, BN) : frag_row(st + P_BYTES, qa, i, h);
+            else pf[h][i - FN] = PS ? frag_tr(st, pa, i - FN, h, BM) : frag_row(st, pa, i - FN, h);
+        };
+        // One half's products, row of sub-tiles by row, with the other half's reads and the copies
+        // dealt out between the rows, so that neither the LDS nor the memory pipeline's queue
+        // ever holds up the matrix core.  (The scheduling barriers keep the compiler from
+        // collecting them again.)
+        auto half = [&](auto which, const uint8_t* read_from, uint8_t* copy_to, const Copies* c) DG_DEV_INLINE {
+            constexpr int h = decltype(which)::value;
             int pa = p_frag, qa = q_frag;
             asm volatile("" : "+v"(pa), "+v"(qa));
 #pragma unroll
-            for (int fn = 0; fn < FN; ++fn) qf[h][fn] = QS ? frag_tr(st + P_BYTES, qa, fn, h, BN) : frag_row(st + P_BYTES, qa, fn, h);
-#pragma unroll
-            for (int fm = 0; fm < FM; ++fm) pf[h][fm] = PS ? frag_tr(st, pa, fm, h, BM) : frag_row(st, pa, fm, h);
-        };
-        auto multiply_half = [&](auto half) DG_DEV_INLINE {
-            constexpr int h = decltype(half)::value;
-#pragma unroll
-            for (int fm = 0; fm < FM; ++fm)
+            for (int fm = 0; fm < FM; ++fm) {
 #pragma unroll
                 for (int fn = 0; fn < FN; ++fn) acc[fm][fn] = T::mfma(qf[h][fn], pf[h][fm], acc[fm][fn]);
+                if constexpr (h == 1) {
+#pragma unroll
+                    for (int i = fm * NCOPY / FM; i < (fm + 1) * NCOPY / FM; ++i) copy_one(copy_to, *c, i);
+                }
+                // (a quarter of the rows is left for the last reads to land)
+                constexpr int R = FM > 3 ? FM * 3 / 4 : FM;
+#pragma unroll
+                for (int i = fm * NREAD / R; i < (fm + 1) * NREAD / R && i < NREAD; ++i)
+                    read_one(read_from, pa, qa, 1 - h, i);
+                __builtin_amdgcn_sched_barrier(0);
+            }
         };
 
         // ---- contraction.  The one barrier of a step sits between its halves: by then every
@@ -287,31 +305,27 @@ ragged_gemm_kernel(const RaggedParams p) {
         // step after next, and every wave's copies of the next step have landed, so its
         // first half is read while this step's second half is multiplied. ----
         if (steps > 0) {
+            // Past the last step, copies read nothing and write zeros and reads bring what nobody
+            // uses: the loop has no special last steps.
             constexpr std::integral_constant<int, 0> first{};
             constexpr std::integral_constant<int, 1> second{};
-            constexpr int NCOPY = P_PER + Q_PER;
-            issue(smem0, 0);
-            if (steps > 1) {
-                issue(smem1, 1);
-                wait_vmem<NCOPY>();
-            } else {
-                wait_vmem<0>();
-            }
+            wait_vmem<0>();      // the last tile's copies past its end
+            const Copies c0 = copies_of(0), c1 = copies_of(1);
+#pragma unroll
+            for (int i = 0; i < NCOPY; ++i) copy_one(smem0, c0, i);
+#pragma unroll
+            for (int i = 0; i < NCOPY; ++i) copy_one(smem1, c1, i);
+            wait_vmem<NCOPY>();
             barrier_only();
-            read_half(smem0, first);
+#pragma unroll
+            for (int i = 0; i < NREAD; ++i) read_one(smem0, p_frag, q_frag, 0, i);
             auto step = [&](int s, uint8_t* cur, uint8_t* next) DG_DEV_INLINE {
-                read_half(cur, second);
-                __builtin_amdgcn_sched_barrier(0);
-                multiply_half(first);
-                __builtin_amdgcn_sched_barrier(0);
+                half(first, cur, cur, nullptr);
                 wait_vmem<0>();
                 wait_lds();
                 barrier_only();
-                if (s + 2 < steps) issue(cur, s + 2);
-                if (s + 1 < steps) read_half(next, first);
-                __builtin_amdgcn_sched_barrier(0);
-                multiply_half(second);
-                __builtin_amdgcn_sched_barrier(0);
+                const Copies c = copies_of(s + 2);
+                half(second, next, cur, &c);
             };
             for (int s = 0; s < steps; s += 2) {
                 step(s, smem0, smem1);
