@@ -33,15 +33,22 @@ __device__ __forceinline__ void unroll(F&& f) {
 // past the end reads zeros and touches no memory.  No descriptor reaches 2^31 bytes and the
 // callers keep every offset below that, so kOutside, plus any of them, is outside of each.
 constexpr uint32_t kOutside = 0x80000000u;
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_over(const void* base, long bytes) {
-    const unsigned n = bytes <= 0 ? 0u : (bytes >= 0x7FFFFFFFl ? 0x7FFFFFFFu : (unsigned)bytes);
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, (int)n, 0x00020000);
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_over(const void* base, int bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, bytes, 0x00020000);
 }
 
 // 16 bytes per lane from a buffer into LDS: lane l's land at dst + 16 l.
 template <int CPOL = 0>
 __device__ __forceinline__ void copy_to_lds16(__amdgpu_buffer_rsrc_t rs, lds_void* dst, uint32_t voff, uint32_t soff) {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, dst, 16, (int)voff, (int)soff, 0, CPOL);
+}
+
+// The lane's number, counted each time: no register holds it in between, and the compiler does
+// not see that it is always the same.
+__device__ __forceinline__ uint32_t lane_now() {
+    uint32_t l;
+    asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=v"(l));
+    return l;
 }
 
 // Workgroup barrier without the memory fence of __syncthreads(), which would also drain

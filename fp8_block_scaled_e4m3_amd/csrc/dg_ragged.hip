@@ -67,18 +67,17 @@ __device__ __forceinline__ void unpack2(uint32_t w, float& x, float& y) {
 // four that pair rows 0-3 and 12-15 of one chunk with rows 4-11 of its neighbour.  This one
 // keeps those sixteen, as well as any sixteen lanes in order, in distinct banks (an earlier one
 // that did only the latter doubled the reads' time: 4 conflict cycles in 8).
-__device__ __forceinline__ int swz_row(int row) { return (row >> 1) & 7; }
+__device__ __forceinline__ uint32_t swz_row(uint32_t row) { return (row >> 1) & 7; }
 // Strided operand: 32-byte unit of a row of one c.  Half a wave's transposing read covers
 // four consecutive c in each of two groups eight apart: eight rows, eight distinct units.
-__device__ __forceinline__ int swz_c(int c) { return (c & 3) | (((c >> 3) & 1) << 2); }
+__device__ __forceinline__ uint32_t swz_c(uint32_t c) { return (c & 3) | (((c >> 3) & 1) << 2); }
 
 // Tile r of a group of ni x nj tiles: bands of kBand row tiles, down a band's column before
 // the next column.  The 32 tiles that an XCD works on at a time are then a block of 8 x 4,
 // whose operands its L2 fetches once.
 constexpr int kBand = 8;
-__device__ __forceinline__ void band_order(long r, int ni, int nj, int& ti, int& tj) {
-    const int band = (int)(r / ((long)kBand * nj));
-    const int rest = (int)(r - (long)band * kBand * nj), height = min(kBand, ni - band * kBand);
+__device__ __forceinline__ void band_order(int r, int ni, int nj, int& ti, int& tj) {
+    const int band = r / (kBand * nj), rest = r - band * (kBand * nj), height = min(kBand, ni - band * kBand);
     ti = band * kBand + rest % height;
     tj = rest / height;
 }
@@ -106,7 +105,6 @@ ragged_gemm_kernel(const RaggedParams p) {
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave % WM, wn = wave / WM;
-    const int l16 = lane & 15, lgrp = lane >> 4;
     const int G = p.groups;
 
     // ---- segments: s_off[g] = the largest of offsets[0..g], clamped to [0, rows], so that
@@ -130,9 +128,9 @@ ragged_gemm_kernel(const RaggedParams p) {
             }
     }
     __syncthreads();
-    long total;
+    int total;                         // (the host keeps its bound below 2^30)
     if constexpr (OP == kRaggedTN) {
-        total = (long)G * p.tiles_i * p.tiles_j;
+        total = G * p.tiles_i * p.tiles_j;
     } else {
         if (wave == 0) {
             const int per = (G + 63) / 64, g0 = lane * per;
@@ -153,7 +151,7 @@ ragged_gemm_kernel(const RaggedParams p) {
             if (lane == 63) s_tiles[G] = incl;
         }
         __syncthreads();
-        total = (long)s_tiles[G] * p.tiles_j;
+        total = __builtin_amdgcn_readfirstlane(s_tiles[G]) * p.tiles_j;
     }
 
     // ---- a lane's place in its copies.  A copy is 1 KiB of a stage: 8 rows of 128 bytes
@@ -162,204 +160,281 @@ ragged_gemm_kernel(const RaggedParams p) {
     // by a whole number of rows. ----
     constexpr int P_RPS = PS ? 512 / BM : 8, Q_RPS = QS ? 512 / BN : 8;
     static_assert(NW * P_RPS % 16 == 0 && NW * Q_RPS % 16 == 0, "the swizzles' period");
-    const int p_row = wave * P_RPS + lane / (64 / P_RPS), q_row = wave * Q_RPS + lane / (64 / Q_RPS);
-    const int p_chunk = (lane % (64 / P_RPS)) ^ (PS ? swz_c(p_row) * 2 : swz_row(p_row));
-    const int q_chunk = (lane % (64 / Q_RPS)) ^ (QS ? swz_c(q_row) * 2 : swz_row(q_row));
-    const uint32_t p_lane = (uint32_t)(p_row * p.ldp + p_chunk * 8) * 2u, q_lane = (uint32_t)(q_row * p.ldq + q_chunk * 8) * 2u;
     const uint32_t p_next = (uint32_t)(NW * P_RPS * p.ldp) * 2u, q_next = (uint32_t)(NW * Q_RPS * p.ldq) * 2u;
 
-    // ---- a lane's place in its fragments: byte offset in an operand's part of a stage of
-    // sub-tile 0 of half 0; strided operands add (xor) the sub-tile's 32-byte unit to it, and
-    // constants lead to the other sub-tiles and halves ----
-    const int tr_c = lgrp * 8 + (l16 >> 2), tr_swz = swz_c(tr_c);
-    const int p_frag = PS ? tr_c * BM * 2 + ((wm * (WTM / 16)) ^ tr_swz) * 32 + (l16 & 3) * 8
-                          : (wm * WTM + l16) * 128 + (lgrp ^ swz_row(l16)) * 16;
-    const int q_frag = QS ? tr_c * BN * 2 + ((wn * (WTN / 16)) ^ tr_swz) * 32 + (l16 & 3) * 8
-                          : (wn * WTN + l16) * 128 + (lgrp ^ swz_row(l16)) * 16;
-
-    for (long L0 = 0; L0 < total; L0 += gridDim.x) {
+    // ---- a tile, all of it wave-uniform: group, first row and column of D (i0 from the segment's
+    // first row seg0 in nt and nn), rows of the segment, contraction length ----
+    struct Tile {
+        int g, i0, j0, seg0, seg_rows, nc;
+        const uint16_t *pb, *qb;   // operands: the tile's first row (contiguous), or c = 0 at its
+    };                             // first column (strided)
+    // Steps of a tile: an even number and at least two.  Steps past the contraction's end (one
+    // at most, but for a group without rows) copy nothing and add zeros, and in exchange a tile
+    // always begins in stage 0 and the loop needs no special cases.
+    auto steps_of = [&](const Tile& t) DG_DEV_INLINE { return max((t.nc + 2 * kStep - 1) / (2 * kStep), 1) * 2; };
+    int next_tile = 0;
+    {
         const int P = gridDim.x, w = blockIdx.x;
         // neighbouring tiles to the workgroups of one XCD (they share its L2)
-        const long L = L0 + (P % kXcdCount == 0 ? (w % kXcdCount) * (P / kXcdCount) + w / kXcdCount : w);
-        if (L >= total) continue;      // uniform
-
-        // ---- the tile: group, first i and j, rows of the segment ----
-        int g, i0, j0, seg0, seg_rows;
+        next_tile = P % kXcdCount == 0 ? (w % kXcdCount) * (P / kXcdCount) + w / kXcdCount : w;
+    }
+    constexpr int D_SIZE = OUT32 ? 4 : 2;
+    // the workgroup's next tile; past the last one a tile that copies nothing
+    auto fetch_tile = [&](Tile& t) DG_DEV_INLINE -> bool {
+        const bool some = next_tile < total;
+        const int L = some ? next_tile : 0;
+        next_tile = some ? next_tile + (int)gridDim.x : next_tile;   // (total + grid fits an int)
+        int g, ti, tj;
         if constexpr (OP == kRaggedTN) {
             const int per = p.tiles_i * p.tiles_j;
-            g = (int)(L / per);
-            int ti, tj;
-            band_order((int)(L - (long)g * per), p.tiles_i, p.tiles_j, ti, tj);
-            i0 = ti * BM;
-            j0 = tj * BN;
+            g = L / per;
+            band_order(L - g * per, p.tiles_i, p.tiles_j, ti, tj);
         } else {
-            const int q = (int)(L / p.tiles_j);
-            int lo = 0, hi = G;        // the last g with s_tiles[g] <= q
+            const int q = L / p.tiles_j;
+            int lo = 0, hi = G;             // the last g with s_tiles[g] <= q
             while (hi - lo > 1) {
                 const int mid = (lo + hi) >> 1;
                 if (s_tiles[mid] <= q) lo = mid; else hi = mid;
             }
             g = lo;
-            const int rt = s_tiles[g + 1] - s_tiles[g];
-            int ti, tj;
-            band_order(L - (long)s_tiles[g] * p.tiles_j, rt, p.tiles_j, ti, tj);
-            i0 = ti * BM;
-            j0 = tj * BN;
+            band_order(L - s_tiles[g] * p.tiles_j, max(s_tiles[g + 1] - s_tiles[g], 1), p.tiles_j, ti, tj);
         }
-        g = __builtin_amdgcn_readfirstlane(g);
-        i0 = __builtin_amdgcn_readfirstlane(i0);
-        j0 = __builtin_amdgcn_readfirstlane(j0);
-        seg0 = __builtin_amdgcn_readfirstlane(s_off[g]);
-        seg_rows = __builtin_amdgcn_readfirstlane(s_off[g + 1]) - seg0;
+        t.g = __builtin_amdgcn_readfirstlane(g);
+        t.i0 = __builtin_amdgcn_readfirstlane(ti) * BM;
+        t.j0 = __builtin_amdgcn_readfirstlane(tj) * BN;
+        t.seg0 = __builtin_amdgcn_readfirstlane(s_off[t.g]);
+        t.seg_rows = __builtin_amdgcn_readfirstlane(s_off[t.g + 1]) - t.seg0;
+        t.nc = some ? (OP == kRaggedTN ? t.seg_rows : p.nc) : 0;
+        t.pb = p.p + (PS ? (long)t.seg0 * p.ldp + t.i0 : (long)(t.seg0 + t.i0) * p.ldp);
+        t.qb = p.q + (OP == kRaggedTN ? (long)t.seg0 * p.ldq + t.j0
+                                      : (long)t.g * p.q_gstride + (QS ? (long)t.j0 : (long)t.j0 * p.ldq));
+        return some;
+    };
 
-        const int ni = OP == kRaggedTN ? p.ni : seg_rows;
-        const int nc = OP == kRaggedTN ? seg_rows : p.nc;
-        const int steps = (nc + kStep - 1) / kStep;
-        // base of P: its first row of the tile (contiguous) or of c = 0, at column i0 (strided)
-        const uint16_t* pb = p.p + (PS ? (long)seg0 * p.ldp + i0 : (long)(seg0 + i0) * p.ldp);
-        const uint16_t* qb = p.q + (OP == kRaggedTN ? (long)seg0 * p.ldq + j0
-                                    : QS ? (long)g * p.q_gstride + j0
-                                         : (long)g * p.q_gstride + (long)j0 * p.ldq);
-        const uint32_t p_off = PS && i0 + p_chunk * 8 >= p.ni ? kOutside : p_lane;
-        const uint32_t q_off = QS && j0 + q_chunk * 8 >= p.nj ? kOutside : q_lane;
-        // contiguous operands: one descriptor for the tile, the step in the scalar offset, the
-        // contraction's end by lane; strided ones: a descriptor per step, over the rows left
-        const long p_bytes = (long)min(ni - i0, BM) * p.ldp * 2, q_bytes = (long)min(p.nj - j0, BN) * p.ldq * 2;
-        struct Copies { __amdgpu_buffer_rsrc_t pr, qr; uint32_t po, qo, soff; };
-        auto copies_of = [&](int s) DG_DEV_INLINE -> Copies {
-            const int c0 = s * kStep, left = nc - c0;
-            const bool some = left > 0, tail = left < kStep;
-            return Copies{PS ? buffer_over(pb + (long)c0 * p.ldp, (long)min(left, kStep) * p.ldp * 2)
-                             : buffer_over(pb, some ? p_bytes : 0),
-                          QS ? buffer_over(qb + (long)c0 * p.ldq, (long)min(left, kStep) * p.ldq * 2)
-                             : buffer_over(qb, some ? q_bytes : 0),
-                          !PS && tail && p_chunk * 8 >= left ? kOutside : p_off,
-                          !QS && tail && q_chunk * 8 >= left ? kOutside : q_off, some ? (uint32_t)c0 * 2u : 0u};
-        };
-        auto copy_one = [&](uint8_t* st, const Copies& c, int i) DG_DEV_INLINE {
-            if (i < P_PER) {
-                copy_to_lds16(c.pr, (lds_void*)(st + (wave + i * NW) * 1024), c.po + i * p_next, PS ? 0u : c.soff);
-            } else {
-                i -= P_PER;
-                copy_to_lds16(c.qr, (lds_void*)(st + P_BYTES + (wave + i * NW) * 1024), c.qo + i * q_next, QS ? 0u : c.soff);
+    // ---- where the copies are: a step of a tile, two steps ahead of the products.  Contiguous
+    // operands: a descriptor over the tile's rows, the step in the scalar offset, the
+    // contraction's end kept by lane; strided ones: a descriptor over the step's rows, the
+    // last column kept by lane ----
+    struct Cursor {
+        const uint16_t *pb, *qb;
+        int left;                  // c from this step to the contraction's end
+        int p_rows, q_rows;        // contiguous: rows of the tile
+        int p_cols, q_cols;        // strided: columns from the tile's first to the matrix's end
+        uint32_t soff;
+    };
+    auto cursor_at = [&](const Tile& t) DG_DEV_INLINE -> Cursor {
+        const int ni = OP == kRaggedTN ? p.ni : t.seg_rows;
+        return Cursor{t.pb, t.qb, t.nc, min(ni - t.i0, BM), min(p.nj - t.j0, BN), ni - t.i0, p.nj - t.j0, 0};
+    };
+    // the step after this one, of the same tile or (`over`) the next tile's first
+    auto advance = [&](Cursor& c, bool over, const Cursor& n) DG_DEV_INLINE {
+        auto pick = [&](int of_next, int of_this) DG_DEV_INLINE { return __builtin_amdgcn_readfirstlane(over ? of_next : of_this); };
+        const uint16_t* pb = PS ? c.pb + kStep * p.ldp : c.pb;
+        const uint16_t* qb = QS ? c.qb + kStep * p.ldq : c.qb;
+        c.pb = over ? n.pb : pb;
+        c.qb = over ? n.qb : qb;
+        c.left = pick(n.left, c.left - kStep);
+        c.p_rows = pick(n.p_rows, c.p_rows);
+        c.q_rows = pick(n.q_rows, c.q_rows);
+        c.p_cols = pick(n.p_cols, c.p_cols);
+        c.q_cols = pick(n.q_cols, c.q_cols);
+        c.soff = pick(0, c.soff + kStep * 2);
+    };
+    struct Copies { __amdgpu_buffer_rsrc_t pr, qr; uint32_t po, qo, soff; };
+    auto copies_at = [&](const Cursor& c) DG_DEV_INLINE -> Copies {
+        // (read from a lane: the clamp is a vector instruction, and descriptors are scalar)
+        const int c_rows = __builtin_amdgcn_readfirstlane(max(min(c.left, kStep), 0));
+        const bool some = c.left > 0;
+        // (from the lane number each time: held across the loop, these offsets would push
+        // accumulators out of the register file)
+        const uint32_t l = lane_now();
+        const uint32_t p_row = wave * P_RPS + l / (64 / P_RPS), q_row = wave * Q_RPS + l / (64 / Q_RPS);
+        const uint32_t p_chunk = (l % (64 / P_RPS)) ^ (PS ? swz_c(p_row) * 2 : swz_row(p_row));
+        const uint32_t q_chunk = (l % (64 / Q_RPS)) ^ (QS ? swz_c(q_row) * 2 : swz_row(q_row));
+        const uint32_t p_lane = (p_row * (uint32_t)p.ldp + p_chunk * 8) * 2, q_lane = (q_row * (uint32_t)p.ldq + q_chunk * 8) * 2;
+        return Copies{buffer_over(c.pb, (PS ? c_rows : some ? c.p_rows : 0) * (int)p.ldp * 2),
+                      buffer_over(c.qb, (QS ? c_rows : some ? c.q_rows : 0) * (int)p.ldq * 2),
+                      (int)p_chunk * 8 >= (PS ? c.p_cols : c.left) ? kOutside : p_lane,
+                      (int)q_chunk * 8 >= (QS ? c.q_cols : c.left) ? kOutside : q_lane, some ? c.soff : 0u};
+    };
+    // Addresses in a stage are one integer offset from its array: through longer chains the
+    // compiler loses track of which stage a read touches, and makes it wait for the copies in
+    // flight into the other.
+    auto copy_one = [&](lds_u8* st, const Copies& c, int i) DG_DEV_INLINE {
+        if (i < P_PER) {
+            copy_to_lds16(c.pr, (lds_void*)(st + (wave + i * NW) * 1024), c.po + i * p_next, PS ? 0u : c.soff);
+        } else {
+            i -= P_PER;
+            copy_to_lds16(c.qr, (lds_void*)(st + (P_BYTES + (wave + i * NW) * 1024)), c.qo + i * q_next, QS ? 0u : c.soff);
+        }
+    };
+
+    // A lane's place in its fragments: byte offset in an operand's part of a stage of sub-tile 0
+    // of half 0.  Strided operands add (xor) the sub-tile's 32-byte unit to it; constants
+    // lead to the other sub-tiles and halves.
+    auto frag_places = [&](uint32_t l, uint32_t& pa, uint32_t& qa) DG_DEV_INLINE {
+        const uint32_t l16 = l % 16, lgrp = l / 16, tr_c = lgrp * 8 + l16 / 4;
+        pa = PS ? tr_c * BM * 2 + ((wm * (WTM / 16)) ^ swz_c(tr_c)) * 32 + l16 % 4 * 8
+                : (wm * WTM + l16) * 128 + (lgrp ^ swz_row(l16)) * 16;
+        qa = QS ? tr_c * BN * 2 + ((wn * (WTN / 16)) ^ swz_c(tr_c)) * 32 + l16 % 4 * 8
+                : (wn * WTN + l16) * 128 + (lgrp ^ swz_row(l16)) * 16;
+    };
+    uint32_t p_frag, q_frag;
+    frag_places(lane, p_frag, q_frag);
+    // Fragment of sub-tile f, half h, of the operand whose part of the stage begins at `part`.
+    auto frag_row = [&](lds_u8* st, uint32_t part, uint32_t at, int f, int h) DG_DEV_INLINE -> v4i {
+        typedef __attribute__((address_space(3))) const v4i lds_v4i;
+        return *(lds_v4i*)(st + (part + (at ^ (h * 64)) + f * 2048));
+    };
+    auto frag_tr = [&](lds_u8* st, uint32_t part, uint32_t at, int f, int h, int width) DG_DEV_INLINE -> v4i {
+        typedef short v4s __attribute__((ext_vector_type(4)));
+        typedef __attribute__((address_space(3))) v4s lds_v4s;
+        const uint32_t o = part + (at ^ (f * 32)) + h * 32 * width * 2;
+        const v2i lo = __builtin_bit_cast(v2i, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(st + o)));
+        const v2i hi = __builtin_bit_cast(v2i, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(st + (o + 4 * width * 2))));
+        return v4i{lo.x, lo.y, hi.x, hi.y};
+    };
+
+    // fragments of half h of a step: one set is multiplied while the other is read
+    v4f acc[FM][FN];
+    v4i pf[2][FM], qf[2][FN];
+    constexpr int NREAD = FM + FN, NCOPY = P_PER + Q_PER;
+    // read i of a half, in the order in which the products need them
+    auto read_one = [&](lds_u8* st, uint32_t pa, uint32_t qa, int h, int i) DG_DEV_INLINE {
+        if (i < FN) qf[h][i] = QS ? frag_tr(st, P_BYTES, qa, i, h, BN) : frag_row(st, P_BYTES, qa, i, h);
+        else pf[h][i - FN] = PS ? frag_tr(st, 0, pa, i - FN, h, BM) : frag_row(st, 0, pa, i - FN, h);
+    };
+    // One half's products, row of sub-tiles by row, with the other half's reads and the copies
+    // dealt out between the rows, so that neither the LDS nor the memory pipeline's queue
+    // ever holds up the matrix core.  (The scheduling barriers keep the compiler from
+    // collecting them again.)
+    auto half = [&](auto which, lds_u8* read_from, lds_u8* copy_to, const Copies* c, auto&& between) DG_DEV_INLINE {
+        constexpr int h = decltype(which)::value;
+        // (hidden at each use: the compiler would otherwise keep one register for every fragment of
+        // every stage, and take the addresses apart)
+        uint32_t pa = p_frag, qa = q_frag;
+        if constexpr (PS) frag_places(lane_now(), pa, qa);   // (no register to spare across the loop)
+        asm volatile("" : "+v"(pa), "+v"(qa));
+#pragma unroll
+        for (int fm = 0; fm < FM; ++fm) {
+#pragma unroll
+            for (int fn = 0; fn < FN; ++fn) acc[fm][fn] = T::mfma(qf[h][fn], pf[h][fm], acc[fm][fn]);
+            if constexpr (h == 1) {
+#pragma unroll
+                for (int i = fm * NCOPY / FM; i < (fm + 1) * NCOPY / FM; ++i) copy_one(copy_to, *c, i);
             }
-        };
+            // (a quarter of the rows is left for the last reads to land)
+            constexpr int R = FM > 3 ? FM * 3 / 4 : FM;
+#pragma unroll
+            for (int i = fm * NREAD / R; i < (fm + 1) * NREAD / R && i < NREAD; ++i)
+                read_one(read_from, pa, qa, 1 - h, i);
+            if (fm == FM / 2) between();
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
 
-        // Fragment of sub-tile f, half h.  The lane's offset is hidden from the compiler at each
-        // use, so that it computes the few addresses it needs (one xor or a constant offset
-        // each) instead of keeping one register for every fragment of every stage.
-        auto frag_row = [&](const uint8_t* b, int at, int f, int h) DG_DEV_INLINE -> v4i {
-            typedef __attribute__((address_space(3))) const v4i lds_v4i;
-            return *(lds_v4i*)((const lds_u8*)b + ((at ^ (h * 64)) + f * 2048));
-        };
-        auto frag_tr = [&](const uint8_t* b, int at, int f, int h, int width) DG_DEV_INLINE -> v4i {
-            typedef short v4s __attribute__((ext_vector_type(4)));
-            typedef __attribute__((address_space(3))) v4s lds_v4s;
-            lds_u8* a = (lds_u8*)b + ((at ^ (f * 32)) + h * 32 * width * 2);
-            const v2i lo = __builtin_bit_cast(v2i, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)a));
-            const v2i hi = __builtin_bit_cast(v2i, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(a + 4 * width * 2)));
-            return v4i{lo.x, lo.y, hi.x, hi.y};
-        };
-
-        v4f acc[FM][FN];
+    // ---- the walk over the tiles.  The one barrier of a step sits between its halves: by then
+    // every wave holds the second half's fragments, so the stage is free for the copies of the
+    // step after next, and every wave's copies of the next step have landed, so its first half
+    // is read while this step's second half is multiplied.  The steps after a tile's last two are
+    // the next tile's first: its copies and fragments arrive before this one's epilogue,
+    // whose stores then drain behind the next products. ----
+    lds_u8 *const st0 = (lds_u8*)smem0, *const st1 = (lds_u8*)smem1;
+    constexpr std::integral_constant<int, 0> first{};
+    constexpr std::integral_constant<int, 1> second{};
+    Tile cur, nxt;
+    if (!fetch_tile(cur)) return;      // uniform
+    Cursor at = cursor_at(cur);
+    {
+        const Copies c0 = copies_at(at);
+#pragma unroll
+        for (int i = 0; i < NCOPY; ++i) copy_one(st0, c0, i);
+        advance(at, false, at);
+        const Copies c1 = copies_at(at);
+#pragma unroll
+        for (int i = 0; i < NCOPY; ++i) copy_one(st1, c1, i);
+        wait_vmem<0>();
+        barrier_only();
+        uint32_t pa = p_frag, qa = q_frag;
+        asm volatile("" : "+v"(pa), "+v"(qa));
+#pragma unroll
+        for (int i = 0; i < NREAD; ++i) read_one(st0, pa, qa, 0, i);
+    }
+    for (;;) {
+        const bool more = fetch_tile(nxt);
 #pragma unroll
         for (int fm = 0; fm < FM; ++fm)
 #pragma unroll
             for (int fn = 0; fn < FN; ++fn) acc[fm][fn] = v4f{0.f, 0.f, 0.f, 0.f};
-
-        // fragments of half h of a step: one set is multiplied while the other is read
-        v4i pf[2][FM], qf[2][FN];
-        constexpr int NREAD = FM + FN, NCOPY = P_PER + Q_PER;
-        // read i of a half, in the order in which the products need them
-        auto read_one = [&](const uint8_t* st, int pa, int qa, int h, int i) DG_DEV_INLINE {
-            if (i < FN) qf[h][i] = QS ? frag_tr(st + P_BYTES, qa, i, h, BN) : frag_row(st + P_BYTES, qa, i, h);
-            else pf[h][i - FN] = PS ? frag_tr(st, pa, i - FN, h, BM) : frag_row(st, pa, i - FN, h);
-        };
-        // One half's products, row of sub-tiles by row, with the other half's reads and the copies
-        // dealt out between the rows, so that neither the LDS nor the memory pipeline's queue
-        // ever holds up the matrix core.  (The scheduling barriers keep the compiler from
-        // collecting them again.)
-        auto half = [&](auto which, const uint8_t* read_from, uint8_t* copy_to, const Copies* c) DG_DEV_INLINE {
-            constexpr int h = decltype(which)::value;
-            int pa = p_frag, qa = q_frag;
-            asm volatile("" : "+v"(pa), "+v"(qa));
-#pragma unroll
-            for (int fm = 0; fm < FM; ++fm) {
-#pragma unroll
-                for (int fn = 0; fn < FN; ++fn) acc[fm][fn] = T::mfma(qf[h][fn], pf[h][fm], acc[fm][fn]);
-                if constexpr (h == 1) {
-#pragma unroll
-                    for (int i = fm * NCOPY / FM; i < (fm + 1) * NCOPY / FM; ++i) copy_one(copy_to, *c, i);
-                }
-                // (a quarter of the rows is left for the last reads to land)
-                constexpr int R = FM > 3 ? FM * 3 / 4 : FM;
-#pragma unroll
-                for (int i = fm * NREAD / R; i < (fm + 1) * NREAD / R && i < NREAD; ++i)
-                    read_one(read_from, pa, qa, 1 - h, i);
-                __builtin_amdgcn_sched_barrier(0);
-            }
-        };
-
-        // ---- contraction.  The one barrier of a step sits between its halves: by then every
-        // wave holds the second half's fragments, so the stage is free for the copies of the
-        // step after next, and every wave's copies of the next step have landed, so its
-        // first half is read while this step's second half is multiplied. ----
-        if (steps > 0) {
-            // Past the last step, copies read nothing and write zeros and reads bring what nobody
-            // uses: the loop has no special last steps.
-            constexpr std::integral_constant<int, 0> first{};
-            constexpr std::integral_constant<int, 1> second{};
-            wait_vmem<0>();      // the last tile's copies past its end
-            const Copies c0 = copies_of(0), c1 = copies_of(1);
-#pragma unroll
-            for (int i = 0; i < NCOPY; ++i) copy_one(smem0, c0, i);
-#pragma unroll
-            for (int i = 0; i < NCOPY; ++i) copy_one(smem1, c1, i);
-            wait_vmem<NCOPY>();
+        const int steps = steps_of(cur);
+        const Cursor then = cursor_at(nxt);
+        auto nothing = []() DG_DEV_INLINE {};
+        for (int s = 0; s < steps; s += 2) {
+            Copies c;
+            half(first, st0, st0, nullptr, [&]() DG_DEV_INLINE { advance(at, s + 2 >= steps, then); c = copies_at(at); });
+            wait_vmem<0>();
+            wait_lds();
             barrier_only();
-#pragma unroll
-            for (int i = 0; i < NREAD; ++i) read_one(smem0, p_frag, q_frag, 0, i);
-            auto step = [&](int s, uint8_t* cur, uint8_t* next) DG_DEV_INLINE {
-                half(first, cur, cur, nullptr);
-                wait_vmem<0>();
-                wait_lds();
-                barrier_only();
-                const Copies c = copies_of(s + 2);
-                half(second, next, cur, &c);
-            };
-            for (int s = 0; s < steps; s += 2) {
-                step(s, smem0, smem1);
-                if (s + 1 < steps) step(s + 1, smem1, smem0);
-            }
+            half(second, st1, st0, &c, nothing);
+            half(first, st1, st1, nullptr, [&]() DG_DEV_INLINE { advance(at, false, at); c = copies_at(at); });
+            wait_vmem<0>();
+            wait_lds();
+            barrier_only();
+            half(second, st0, st1, &c, nothing);
         }
 
-        // ---- epilogue: lane l16 holds row l16 of a sub-tile, columns 4 lgrp .. + 3 ----
-        const int rows_left = ni - i0;
+        // ---- epilogue: lane l16 holds row l16 of a sub-tile, columns 4 lgrp .. + 3.  Stores go
+        // through a descriptor over the tile's rows, so that every lane takes part in each
+        // (the count above) and those outside write nothing. ----
+        uint8_t* const d_tile = (uint8_t*)p.d + (OP == kRaggedTN ? (long)cur.g * p.d_gstride + (long)cur.i0 * p.ldd
+                                                                 : (long)(cur.seg0 + cur.i0) * p.ldd) * D_SIZE;
+        const int d_rows = min((OP == kRaggedTN ? p.ni : cur.seg_rows) - cur.i0, BM);
+        const __amdgpu_buffer_rsrc_t dr = buffer_over(d_tile, d_rows * (int)p.ldd * D_SIZE);
+        const int el = lane_now(), e16 = el & 15, egrp = el >> 4;
+        const uint32_t d_lane = (uint32_t)((wm * WTM + e16) * (int)p.ldd) * D_SIZE;
+        auto d_off = [&](int fm, int col) DG_DEV_INLINE -> uint32_t {
+            return col < p.nj ? d_lane + (uint32_t)(fm * 16 * (int)p.ldd + col) * D_SIZE : kOutside;
+        };
+        typedef unsigned v4u __attribute__((ext_vector_type(4)));
+        const bool add = OP == kRaggedTN && p.accumulate;
+        if constexpr (OUT32) {
+            const int col0 = cur.j0 + wn * WTN + egrp * 4;
+            v4u old[2][FN];
+            auto load_row = [&](int fm) DG_DEV_INLINE {
 #pragma unroll
-        for (int fm = 0; fm < FM; ++fm) {
-            const int li = wm * WTM + fm * 16 + l16;
-            const bool row_ok = li < rows_left;
-            const long drow = OP == kRaggedTN ? (long)g * p.d_gstride + (long)(row_ok ? i0 + li : 0) * p.ldd
-                                              : (long)(seg0 + (row_ok ? i0 + li : 0)) * p.ldd;
-            if constexpr (OUT32) {
+                for (int fn = 0; fn < FN; ++fn)
+                    old[fm & 1][fn] = __builtin_amdgcn_raw_buffer_load_b128(dr, (int)d_off(fm, col0 + fn * 16), 0, 0);
+            };
+            if (add) load_row(0);
+#pragma unroll
+            for (int fm = 0; fm < FM; ++fm) {
+                if (add && fm + 1 < FM) load_row(fm + 1);
 #pragma unroll
                 for (int fn = 0; fn < FN; ++fn) {
-                    const int col = j0 + wn * WTN + fn * 16 + lgrp * 4;
-                    if (row_ok && col < p.nj) {
-                        v4f* at = (v4f*)((float*)p.d + drow + col);
-                        *at = p.accumulate ? *at + acc[fm][fn] : acc[fm][fn];
-                    }
+                    v4f x = acc[fm][fn];
+                    if (add) x = __builtin_bit_cast(v4f, old[fm & 1][fn]) + x;
+                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u, x), dr, (int)d_off(fm, col0 + fn * 16), 0, 0);
                 }
-            } else {
-                // the swap of adjacent 16-lane rows gives every lane eight adjacent columns:
-                // group lgrp then holds sub-tile fn + (lgrp & 1), columns 8 (lgrp >> 1) .. + 7
+            }
+        } else {
+            // the swap of adjacent 16-lane rows gives every lane eight adjacent columns: group
+            // lgrp then holds sub-tile fn + (lgrp & 1), columns 8 (lgrp >> 1) .. + 7
+            const int col0 = cur.j0 + wn * WTN + (egrp & 1) * 16 + (egrp >> 1) * 8;
+            v4u old[2][FN / 2];
+            auto load_row = [&](int fm) DG_DEV_INLINE {
+#pragma unroll
+                for (int fn = 0; fn < FN; fn += 2)
+                    old[fm & 1][fn / 2] = __builtin_amdgcn_raw_buffer_load_b128(dr, (int)d_off(fm, col0 + fn * 16), 0, 0);
+            };
+            if (add) load_row(0);
+#pragma unroll
+            for (int fm = 0; fm < FM; ++fm) {
+                if (add && fm + 1 < FM) load_row(fm + 1);
 #pragma unroll
                 for (int fn = 0; fn < FN; fn += 2) {
                     const v4f x = acc[fm][fn], y = acc[fm][fn + 1];
-                    const int col = j0 + wn * WTN + (fn + (lgrp & 1)) * 16 + (lgrp >> 1) * 8;
-                    const bool ok = row_ok && col < p.nj;
-                    uint4* at = (uint4*)((uint16_t*)p.d + drow + (ok ? col : 0));
-                    if (OP == kRaggedTN && p.accumulate) {
+                    v4u w;
+                    if (add) {
                         // the sums are added in fp32 and rounded once: exchange them unrounded
                         float v[8];
 #pragma unroll
@@ -369,26 +444,25 @@ ragged_gemm_kernel(const RaggedParams p) {
                             v[e] = __uint_as_float(sw[0]);
                             v[4 + e] = __uint_as_float(sw[1]);
                         }
-                        if (ok) {
-                            uint4 old = *at;
-                            uint32_t* ow = (uint32_t*)&old;
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                float a, b;
-                                unpack2<T>(ow[e], a, b);
-                                ow[e] = pack2<T>(a + v[2 * e], b + v[2 * e + 1]);
-                            }
-                            *at = old;
+                        for (int e = 0; e < 4; ++e) {
+                            float a, b;
+                            unpack2<T>(old[fm & 1][fn / 2][e], a, b);
+                            w[e] = pack2<T>(a + v[2 * e], b + v[2 * e + 1]);
                         }
                     } else {
                         const auto s0 = __builtin_amdgcn_permlane16_swap(pack2<T>(x[0], x[1]), pack2<T>(y[0], y[1]), false, false);
                         const auto s1 = __builtin_amdgcn_permlane16_swap(pack2<T>(x[2], x[3]), pack2<T>(y[2], y[3]), false, false);
-                        if (ok) *at = uint4{s0[0], s1[0], s0[1], s1[1]};
+                        w = v4u{s0[0], s1[0], s0[1], s1[1]};
                     }
+                    __builtin_amdgcn_raw_buffer_store_b128(w, dr, (int)d_off(fm, col0 + fn * 16), 0, 0);
                 }
             }
         }
+        if (!more) break;              // uniform
+        cur = nxt;
     }
+    wait_vmem<0>();      // no copy into LDS outlives the workgroup
 }
 
 template <typename T, int OP, int BM, int BN, int WM, int WN, bool OUT32>

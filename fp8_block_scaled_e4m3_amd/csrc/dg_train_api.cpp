@@ -18,7 +18,8 @@
 namespace {
 
 constexpr int kMaxConfigs = 64;
-constexpr long kMaxLd = 1l << 22;      // a tile's copies use 31-bit offsets: 256 rows of ld elements
+constexpr long kMaxLd = 1l << 21;      // a tile is addressed with 31-bit offsets: 256 rows of ld fp32 values
+constexpr long kMaxTiles = 1l << 30;   // tile numbers, and one round past the last, are ints
 
 // dg_set_ragged_tile: 0 plans.  Per thread, like dg_set_kernel_config.
 thread_local int g_pinned_bm = 0, g_pinned_bn = 0;
@@ -87,6 +88,7 @@ int launch_ragged(int op, int half, int out_f32, dg::RaggedParams& p, void* stre
     p.tiles_j = (int)ceil_div(p.nj, c.bn);
     long grid = (long)units * blocks_per_cu(&c, best);
     const long tiles = tiles_bound(op, p, c.bm, c.bn);
+    if (tiles >= kMaxTiles) return DG_ERR_UNSUPPORTED;
     if (tiles < grid) grid = tiles;
     if (c.launch(p, (int)grid, static_cast<hipStream_t>(stream)) != hipSuccess) {
         (void)hipGetLastError();

@@ -210,7 +210,7 @@ int dg_quantize_fp8_128x128_fmt(const void* x, int x_dtype, long ldx, int rows, 
  * and d outside every segment (before the first, after the last) are not read and not
  * written.  A row that is NaN or infinite in one group's rows does not reach another's.
  * Requirements: n % 8 == 0, k % 8 == 0, num_groups <= 1024, n, k and leading dimensions
- * below 2^22 (else DG_ERR_UNSUPPORTED); a, b, d 16-byte aligned and leading dimensions
+ * below 2^21 and fewer than 2^30 tiles of d (else DG_ERR_UNSUPPORTED); a, b, d 16-byte aligned and leading dimensions
  * multiples of 8 (else DG_ERR_MISALIGNED); leading dimensions at least the width, non-null
  * pointers for non-empty problems (else DG_ERR_INVALID_ARG).  The contraction must not be
  * empty in the calls with weights (DG_ERR_UNSUPPORTED).  d must not overlap a or b.

@@ -61,7 +61,7 @@ int main() {
     void* const b = (void*)0x2000;
     void* const d = (void*)0x3000;
     const int* off = (const int*)0x4000;
-    const int big = (1 << 22) - 8;
+    const int big = (1 << 21) - 8;
     // the launches of ordinary calls
     expect(dg_m_grouped_gemm_ragged_nt(a, 64, b, d, 136, off, 10, 136, 64, 4, DG_DTYPE_BF16, nullptr) == DG_OK, "nt");
     expect(g_op == 0 && g_half == 0 && g_ragged.tiles_j == 2 && g_ragged.nc == 64 && g_ragged.q_gstride == 136 * 64 &&
@@ -74,11 +74,15 @@ int main() {
     // no row at all: the gradient's zeros are still written
     expect(dg_k_grouped_gemm_ragged_tn(nullptr, 136, nullptr, 64, d, off, 0, 136, 64, 3, DG_DTYPE_BF16, DG_DTYPE_BF16, 0,
                                        nullptr) == DG_OK && g_grid == 6, "tn without rows");
-    // the largest sizes: no product overflows
-    expect(dg_m_grouped_gemm_ragged_nt(a, big, b, d, big, off, INT_MAX, big, big, 1024, DG_DTYPE_BF16, nullptr) == DG_OK &&
-           g_grid == 512, "largest nt");
+    // the largest sizes: no product overflows; too many tiles are refused
+    expect(dg_m_grouped_gemm_ragged_nt(a, big, b, d, big, off, 1 << 20, 2048, big, 1024, DG_DTYPE_BF16, nullptr) == DG_OK &&
+           g_grid == 512, "large nt");
+    expect(dg_m_grouped_gemm_ragged_nt(a, big, b, d, big, off, INT_MAX, big, big, 1024, DG_DTYPE_BF16, nullptr) ==
+           DG_ERR_UNSUPPORTED, "largest nt");
     expect(dg_k_grouped_gemm_ragged_tn(a, big, b, big, d, off, INT_MAX, big, big, 1024, DG_DTYPE_BF16, DG_DTYPE_F32, 1,
-                                       nullptr) == DG_OK && g_grid == 512, "largest tn");
+                                       nullptr) == DG_ERR_UNSUPPORTED, "largest tn");
+    expect(dg_k_grouped_gemm_ragged_tn(a, big, b, big, d, off, INT_MAX, 8192, 8192, 1024, DG_DTYPE_BF16, DG_DTYPE_F32, 1,
+                                       nullptr) == DG_OK && g_grid == 512, "large tn");
     expect(dg_m_grouped_gemm_ragged_nt(a, LONG_MAX, b, d, 136, off, 10, 136, 64, 4, DG_DTYPE_BF16, nullptr) ==
            DG_ERR_UNSUPPORTED, "lda past 63 bits' use");
     const int before = g_launches;

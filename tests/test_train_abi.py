@@ -40,7 +40,7 @@ WEIGHTS = ["dg_m_grouped_gemm_ragged_nt", "dg_m_grouped_gemm_ragged_nn"]
     (dict(dtype=F32), INVALID), (dict(dtype=7), INVALID), (dict(lda=56), INVALID), (dict(ldd=56), INVALID),
     (dict(a=None), INVALID), (dict(b=None), INVALID), (dict(d=None), INVALID), (dict(offsets=None), INVALID),
     (dict(n=60), UNSUPPORTED), (dict(k=100), UNSUPPORTED), (dict(g=1025), UNSUPPORTED),
-    (dict(lda=1 << 22), UNSUPPORTED), (dict(ldd=1 << 22), UNSUPPORTED), (dict(lda=1 << 40), UNSUPPORTED),
+    (dict(lda=1 << 21), UNSUPPORTED), (dict(ldd=1 << 21), UNSUPPORTED), (dict(lda=1 << 40), UNSUPPORTED),
     (dict(a=A + 8), MISALIGNED), (dict(b=B + 2), MISALIGNED), (dict(d=D + 4), MISALIGNED), (dict(lda=132), MISALIGNED),
     (dict(ldd=1028), MISALIGNED), (dict(offsets=OFF + 2), MISALIGNED),
     (dict(m=0), OK), (dict(m=0, a=None), OK)])
@@ -58,7 +58,7 @@ def test_empty_extents(lib):
     (dict(m=-1), INVALID), (dict(g=0), INVALID), (dict(dtype=F32), INVALID), (dict(d_dtype=F16), INVALID),
     (dict(d_dtype=9), INVALID), (dict(accumulate=2), INVALID), (dict(lda=56), INVALID), (dict(ldb=120), INVALID),
     (dict(a=None), INVALID), (dict(b=None), INVALID), (dict(d=None), INVALID), (dict(offsets=None), INVALID),
-    (dict(n=4), UNSUPPORTED), (dict(k=4), UNSUPPORTED), (dict(g=5000), UNSUPPORTED), (dict(ldb=1 << 22), UNSUPPORTED),
+    (dict(n=4), UNSUPPORTED), (dict(k=4), UNSUPPORTED), (dict(g=5000), UNSUPPORTED), (dict(ldb=1 << 21), UNSUPPORTED),
     (dict(a=A + 2), MISALIGNED), (dict(b=B + 8), MISALIGNED), (dict(d=D + 8), MISALIGNED), (dict(ldb=130), MISALIGNED),
     (dict(n=0), OK), (dict(k=0), OK), (dict(m=0, accumulate=1), OK), (dict(m=0, accumulate=1, a=None, b=None), OK)])
 def test_weight_gradient_refuses(lib, change, status):
