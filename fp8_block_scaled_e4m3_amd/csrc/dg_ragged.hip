@@ -100,7 +100,7 @@ ragged_gemm_kernel(const RaggedParams p) {
     __shared__ __attribute__((aligned(1024))) uint8_t smem0[STAGE];
     __shared__ __attribute__((aligned(1024))) uint8_t smem1[STAGE];
     __shared__ int s_off[kMaxRaggedGroups + 1];                              // clamped, non-decreasing
-    __shared__ int s_tiles[OP == kRaggedTN ? 1 : kMaxRaggedGroups + 1];      // row tiles before a group
+    __shared__ int s_tiles[kMaxRaggedGroups + 1];   // nt, nn: row tiles before a group; tn: groups, longest first
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -131,6 +131,18 @@ ragged_gemm_kernel(const RaggedParams p) {
     int total;                         // (the host keeps its bound below 2^30)
     if constexpr (OP == kRaggedTN) {
         total = G * p.tiles_i * p.tiles_j;
+        // Tiles differ in length with their group: they are dealt out longest first, and every
+        // other round backwards, so that the workgroups' sums come out nearly even.
+        for (int g = tid; g < G; g += NW * 64) {
+            const int len = s_off[g + 1] - s_off[g];
+            int rank = 0;
+            for (int h = 0; h < G; ++h) {
+                const int other = s_off[h + 1] - s_off[h];
+                rank += other > len || (other == len && h < g);
+            }
+            s_tiles[rank] = g;
+        }
+        __syncthreads();
     } else {
         if (wave == 0) {
             const int per = (G + 63) / 64, g0 = lane * per;
@@ -172,23 +184,22 @@ ragged_gemm_kernel(const RaggedParams p) {
     // at most, but for a group without rows) copy nothing and add zeros, and in exchange a tile
     // always begins in stage 0 and the loop needs no special cases.
     auto steps_of = [&](const Tile& t) DG_DEV_INLINE { return max((t.nc + 2 * kStep - 1) / (2 * kStep), 1) * 2; };
-    int next_tile = 0;
-    {
-        const int P = gridDim.x, w = blockIdx.x;
-        // neighbouring tiles to the workgroups of one XCD (they share its L2)
-        next_tile = P % kXcdCount == 0 ? (w % kXcdCount) * (P / kXcdCount) + w / kXcdCount : w;
-    }
+    int round = 0, place = blockIdx.x;      // place of the workgroup in a round
+    // (neighbouring tiles to the workgroups of one XCD: they share its L2)
+    if (gridDim.x % kXcdCount == 0) place = place % kXcdCount * (gridDim.x / kXcdCount) + place / kXcdCount;
     constexpr int D_SIZE = OUT32 ? 4 : 2;
     // the workgroup's next tile; past the last one a tile that copies nothing
     auto fetch_tile = [&](Tile& t) DG_DEV_INLINE -> bool {
-        const bool some = next_tile < total;
-        const int L = some ? next_tile : 0;
-        next_tile = some ? next_tile + (int)gridDim.x : next_tile;   // (total + grid fits an int)
+        const int given = round * (int)gridDim.x + (OP == kRaggedTN && (round & 1) ? (int)gridDim.x - 1 - place : place);
+        const bool some = given < total;    // (total + grid fits an int)
+        const int L = some ? given : 0;
+        round += some;
         int g, ti, tj;
         if constexpr (OP == kRaggedTN) {
             const int per = p.tiles_i * p.tiles_j;
-            g = L / per;
-            band_order(L - g * per, p.tiles_i, p.tiles_j, ti, tj);
+            const int rank = L / per;
+            g = s_tiles[rank];
+            band_order(L - rank * per, p.tiles_i, p.tiles_j, ti, tj);
         } else {
             const int q = L / p.tiles_j;
             int lo = 0, hi = G;             // the last g with s_tiles[g] <= q
@@ -360,12 +371,39 @@ ragged_gemm_kernel(const RaggedParams p) {
 #pragma unroll
         for (int i = 0; i < NREAD; ++i) read_one(st0, pa, qa, 0, i);
     }
-    for (;;) {
-        const bool more = fetch_tile(nxt);
+    // D of a tile, for stores and loads that leave out what lies outside: every lane takes part,
+    // with an offset outside the descriptor where its row or column is.
+    typedef unsigned v4u __attribute__((ext_vector_type(4)));
+    auto d_rows_of = [&](const Tile& t, bool some) DG_DEV_INLINE -> __amdgpu_buffer_rsrc_t {
+        uint8_t* const base = (uint8_t*)p.d + (OP == kRaggedTN ? (long)t.g * p.d_gstride + (long)t.i0 * p.ldd
+                                                               : (long)(t.seg0 + t.i0) * p.ldd) * D_SIZE;
+        const int rows = min((OP == kRaggedTN ? p.ni : t.seg_rows) - t.i0, BM);
+        return buffer_over(base, some ? rows * (int)p.ldd * D_SIZE : 0);
+    };
+    const bool add = OP == kRaggedTN && p.accumulate;
+    // fp32 output: lane l holds row l % 16 of a sub-tile, columns 4 (l / 16) .. + 3
+    auto off32 = [&](const Tile& t, uint32_t l, int fm, int fn) DG_DEV_INLINE -> int {
+        const int col = t.j0 + wn * WTN + fn * 16 + l / 16 * 4;
+        const uint32_t o = ((wm * WTM + fm * 16 + l % 16) * (uint32_t)p.ldd + col) * 4;
+        return col < p.nj ? o : kOutside;
+    };
+    // The sums start from zero, or with fp32 output from what D holds: loaded into the accumulators
+    // themselves, all at once (where nothing is to be added, from a descriptor of no bytes,
+    // which gives the zeros).
+    auto start_sums = [&](const Tile& t, bool some) DG_DEV_INLINE {
+        const __amdgpu_buffer_rsrc_t dr = d_rows_of(t, some && add);
+        const uint32_t l = lane_now();
 #pragma unroll
         for (int fm = 0; fm < FM; ++fm)
 #pragma unroll
-            for (int fn = 0; fn < FN; ++fn) acc[fm][fn] = v4f{0.f, 0.f, 0.f, 0.f};
+            for (int fn = 0; fn < FN; ++fn) {
+                if constexpr (OUT32) acc[fm][fn] = __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(dr, off32(t, l, fm, fn), 0, 0));
+                else acc[fm][fn] = v4f{0.f, 0.f, 0.f, 0.f};
+            }
+    };
+    start_sums(cur, true);
+    for (;;) {
+        const bool more = fetch_tile(nxt);
         const int steps = steps_of(cur);
         const Cursor then = cursor_at(nxt);
         auto nothing = []() DG_DEV_INLINE {};
@@ -383,48 +421,29 @@ ragged_gemm_kernel(const RaggedParams p) {
             half(second, st0, st1, &c, nothing);
         }
 
-        // ---- epilogue: lane l16 holds row l16 of a sub-tile, columns 4 lgrp .. + 3.  Stores go
-        // through a descriptor over the tile's rows, so that every lane takes part in each
-        // (the count above) and those outside write nothing. ----
-        uint8_t* const d_tile = (uint8_t*)p.d + (OP == kRaggedTN ? (long)cur.g * p.d_gstride + (long)cur.i0 * p.ldd
-                                                                 : (long)(cur.seg0 + cur.i0) * p.ldd) * D_SIZE;
-        const int d_rows = min((OP == kRaggedTN ? p.ni : cur.seg_rows) - cur.i0, BM);
-        const __amdgpu_buffer_rsrc_t dr = buffer_over(d_tile, d_rows * (int)p.ldd * D_SIZE);
-        const int el = lane_now(), e16 = el & 15, egrp = el >> 4;
-        const uint32_t d_lane = (uint32_t)((wm * WTM + e16) * (int)p.ldd) * D_SIZE;
-        auto d_off = [&](int fm, int col) DG_DEV_INLINE -> uint32_t {
-            return col < p.nj ? d_lane + (uint32_t)(fm * 16 * (int)p.ldd + col) * D_SIZE : kOutside;
-        };
-        typedef unsigned v4u __attribute__((ext_vector_type(4)));
-        const bool add = OP == kRaggedTN && p.accumulate;
+        // ---- epilogue ----
+        const __amdgpu_buffer_rsrc_t dr = d_rows_of(cur, true);
         if constexpr (OUT32) {
-            const int col0 = cur.j0 + wn * WTN + egrp * 4;
-            v4u old[2][FN];
-            auto load_row = [&](int fm) DG_DEV_INLINE {
+            const uint32_t l = lane_now();
+#pragma unroll
+            for (int fm = 0; fm < FM; ++fm)
 #pragma unroll
                 for (int fn = 0; fn < FN; ++fn)
-                    old[fm & 1][fn] = __builtin_amdgcn_raw_buffer_load_b128(dr, (int)d_off(fm, col0 + fn * 16), 0, 0);
-            };
-            if (add) load_row(0);
-#pragma unroll
-            for (int fm = 0; fm < FM; ++fm) {
-                if (add && fm + 1 < FM) load_row(fm + 1);
-#pragma unroll
-                for (int fn = 0; fn < FN; ++fn) {
-                    v4f x = acc[fm][fn];
-                    if (add) x = __builtin_bit_cast(v4f, old[fm & 1][fn]) + x;
-                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u, x), dr, (int)d_off(fm, col0 + fn * 16), 0, 0);
-                }
-            }
+                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u, acc[fm][fn]), dr, off32(cur, l, fm, fn), 0, 0);
         } else {
             // the swap of adjacent 16-lane rows gives every lane eight adjacent columns: group
-            // lgrp then holds sub-tile fn + (lgrp & 1), columns 8 (lgrp >> 1) .. + 7
-            const int col0 = cur.j0 + wn * WTN + (egrp & 1) * 16 + (egrp >> 1) * 8;
+            // l / 16 = q then holds sub-tile fn + (q & 1), columns 8 (q >> 1) .. + 7
+            const uint32_t l = lane_now(), l_grp = l / 16;
+            auto off16 = [&](int fm, int fn) DG_DEV_INLINE -> int {
+                const int col = cur.j0 + wn * WTN + (fn + (l_grp & 1)) * 16 + (l_grp >> 1) * 8;
+                const uint32_t o = ((wm * WTM + fm * 16 + l % 16) * (uint32_t)p.ldd + col) * 2;
+                return col < p.nj ? o : kOutside;
+            };
             v4u old[2][FN / 2];
             auto load_row = [&](int fm) DG_DEV_INLINE {
 #pragma unroll
                 for (int fn = 0; fn < FN; fn += 2)
-                    old[fm & 1][fn / 2] = __builtin_amdgcn_raw_buffer_load_b128(dr, (int)d_off(fm, col0 + fn * 16), 0, 0);
+                    old[fm & 1][fn / 2] = __builtin_amdgcn_raw_buffer_load_b128(dr, off16(fm, fn), 0, 0);
             };
             if (add) load_row(0);
 #pragma unroll
@@ -455,11 +474,12 @@ ragged_gemm_kernel(const RaggedParams p) {
                         const auto s1 = __builtin_amdgcn_permlane16_swap(pack2<T>(x[2], x[3]), pack2<T>(y[2], y[3]), false, false);
                         w = v4u{s0[0], s1[0], s0[1], s1[1]};
                     }
-                    __builtin_amdgcn_raw_buffer_store_b128(w, dr, (int)d_off(fm, col0 + fn * 16), 0, 0);
+                    __builtin_amdgcn_raw_buffer_store_b128(w, dr, off16(fm, fn), 0, 0);
                 }
             }
         }
         if (!more) break;              // uniform
+        start_sums(nxt, true);
         cur = nxt;
     }
     wait_vmem<0>();      // no copy into LDS outlives the workgroup
