@@ -387,38 +387,54 @@ def dg_check_contiguous_layout(m_indices, num_groups: int):
 
 
 # ---- training operators: 16-bit products grouped by expert with ragged segments
+_half_codes = {}     # torch dtype -> DG_DTYPE code, filled at the first call
+
+
 def _half_type(*named):
-    """The 16-bit type all the tensors share, as a DG_DTYPE code (each a GPU tensor with
-    contiguous last dimension)."""
+    """The 16-bit type that all the tensors share, as a DG_DTYPE code (each a GPU tensor with
+    contiguous last dimension).  These calls are short enough for their checks to show: what is
+    in order passes a few comparisons, the rest gets its message from _dev."""
     import torch
-    first = named[0][0]
+    if not _half_codes:
+        _half_codes.update({torch.bfloat16: 1, torch.float16: 2})
+    kind = named[0][0].dtype
     for t, name, ndim in named:
-        _dev(t, name, (torch.bfloat16, torch.float16), ndim)
-        if t.dtype != first.dtype:
-            raise TypeError(f"{name} has dtype {t.dtype}, expected {first.dtype}")
-    return 1 if first.dtype == torch.bfloat16 else 2
+        if t.dtype != kind or not t.is_cuda or t.dim() != ndim or t.stride(-1) != 1 or kind not in _half_codes:
+            _dev(t, name, (torch.bfloat16, torch.float16), ndim)
+            raise TypeError(f"{name} has dtype {t.dtype}, expected {kind}")
+    return _half_codes[kind]
 
 
 def _ragged_offsets(offsets, groups):
     import torch
-    p = _dev(offsets, "offsets", (torch.int32,), 1)
+    if offsets.dtype != torch.int32 or not offsets.is_cuda or offsets.dim() != 1 or offsets.stride(0) != 1:
+        _dev(offsets, "offsets", (torch.int32,), 1)
     if offsets.shape[0] != groups + 1:
         raise ValueError(f"offsets has {offsets.shape[0]} entries, expected {groups + 1}")
-    return p
+    return offsets.data_ptr()
+
+
+def _raw_stream(stream):
+    """As _stream, without building a stream object when none is given (2.5 us)."""
+    import torch
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _ragged_with_weights(call, a, b, d, offsets, transposed, stream):
     dt = _half_type((a, "a", 2), (b, "b", 3), (d, "d", 2))
     groups, n, k = b.shape
-    rows, wa, wd = a.shape[0], n if transposed else k, k if transposed else n
-    if a.shape[1] != wa or tuple(d.shape) != (rows, wd):
+    rows, width = a.shape
+    wa, wd = (n, k) if transposed else (k, n)
+    if width != wa or d.shape != (rows, wd):
         raise ValueError(f"shape mismatch: a {tuple(a.shape)}, b {tuple(b.shape)}, d {tuple(d.shape)}")
     if not b.is_contiguous():
         raise ValueError("b must be contiguous")
     lda, ldd = (a.stride(0), d.stride(0)) if rows > 1 else (wa, wd)
-    _check(getattr(load_library(), call)(a.data_ptr(), lda, b.data_ptr(), d.data_ptr(), ldd,
-                                         _ragged_offsets(offsets, groups), rows, n, k, groups, dt, _stream(stream)),
-           call)
+    _check(getattr(_lib or load_library(), call)(a.data_ptr(), lda, b.data_ptr(), d.data_ptr(), ldd,
+                                                 _ragged_offsets(offsets, groups), rows, n, k, groups, dt,
+                                                 _raw_stream(stream)), call)
 
 
 def dg_m_grouped_gemm_ragged_nt(a, b, d, offsets, stream=None) -> None:
@@ -443,15 +459,14 @@ def dg_k_grouped_gemm_ragged_tn(a, b, d, offsets, accumulate=False, stream=None)
     dt = _half_type((a, "a", 2), (b, "b", 2))
     _dev(d, "d", (a.dtype, torch.float32), 3)
     (rows, n), (groups, dn, k) = a.shape, d.shape
-    if dn != n or tuple(b.shape) != (rows, k):
+    if dn != n or b.shape != (rows, k):
         raise ValueError(f"shape mismatch: a {tuple(a.shape)}, b {tuple(b.shape)}, d {tuple(d.shape)}")
     if not d.is_contiguous():
         raise ValueError("d must be contiguous")
     lda, ldb = (a.stride(0), b.stride(0)) if rows > 1 else (n, k)
-    _check(load_library().dg_k_grouped_gemm_ragged_tn(a.data_ptr(), lda, b.data_ptr(), ldb, d.data_ptr(),
-                                                      _ragged_offsets(offsets, groups), rows, n, k, groups, dt,
-                                                      0 if d.dtype == torch.float32 else dt, int(bool(accumulate)),
-                                                      _stream(stream)), "dg_k_grouped_gemm_ragged_tn")
+    _check((_lib or load_library()).dg_k_grouped_gemm_ragged_tn(
+        a.data_ptr(), lda, b.data_ptr(), ldb, d.data_ptr(), _ragged_offsets(offsets, groups), rows, n, k, groups, dt,
+        0 if d.dtype == torch.float32 else dt, int(bool(accumulate)), _raw_stream(stream)), "dg_k_grouped_gemm_ragged_tn")
 
 
 # ---- training operators: an AdamW step over many tensors at once
@@ -549,7 +564,7 @@ def dg_adamw_step(plan, step, lr, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay
             raise ValueError("grad_scale must hold one value")
     _check(load_library().dg_adamw_step(plan.table.data_ptr(), plan.count, plan.table.numel(), step, lr, beta1, beta2,
                                         eps, weight_decay, None if grad_scale is None else grad_scale.data_ptr(),
-                                        _stream(stream)), "dg_adamw_step")
+                                        _raw_stream(stream)), "dg_adamw_step")
 
 
 # ---- the README's Python names ("deepseek-ai/deepgemm: clean and efficient FP8 GEMM

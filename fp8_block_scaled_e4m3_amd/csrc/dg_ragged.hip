@@ -82,6 +82,58 @@ __device__ __forceinline__ void band_order(int r, int ni, int nj, int& ti, int& 
     tj = rest / height;
 }
 
+// One wave: s_off[g] = the largest of offsets[0..g], clamped to [0, rows], so that no offsets,
+// whatever they hold, lead outside the operands.
+__device__ __forceinline__ void read_segments(const RaggedParams& p, int lane, int* s_off) {
+    const int G = p.groups, per = (G + 1 + 63) / 64, g0 = lane * per;
+    int top = 0;
+    for (int i = 0; i < per; ++i)
+        if (g0 + i <= G) top = max(top, min(p.offsets[g0 + i], p.rows));
+    for (int d = 1; d < 64; d <<= 1) {
+        const int v = __shfl_up(top, d, 64);
+        if (lane >= d) top = max(top, v);
+    }
+    int before = __shfl_up(top, 1, 64);
+    if (lane == 0) before = 0;
+    for (int i = 0; i < per; ++i)
+        if (g0 + i <= G) {
+            before = max(before, min(p.offsets[g0 + i], p.rows));
+            s_off[g0 + i] = before;
+        }
+}
+
+// The same wave: row tiles of the groups before each, s_tiles[groups] being all of them.
+template <int BM>
+__device__ __forceinline__ void count_row_tiles(int G, int lane, const int* s_off, int* s_tiles) {
+    const int per = (G + 63) / 64, g0 = lane * per;
+    asm volatile("" ::: "memory");      // (one wave's LDS accesses complete in order)
+    int own = 0;
+    for (int i = 0; i < per; ++i)
+        if (g0 + i < G) own += (s_off[g0 + i + 1] - s_off[g0 + i] + BM - 1) / BM;
+    int incl = own;
+    for (int d = 1; d < 64; d <<= 1) {
+        const int v = __shfl_up(incl, d, 64);
+        if (lane >= d) incl += v;
+    }
+    int run = incl - own;
+    for (int i = 0; i < per; ++i)
+        if (g0 + i < G) {
+            s_tiles[g0 + i] = run;
+            run += (s_off[g0 + i + 1] - s_off[g0 + i] + BM - 1) / BM;
+        }
+    if (lane == 63) s_tiles[G] = incl;
+}
+
+// The group of row tile q: the last g with s_tiles[g] <= q.
+__device__ __forceinline__ int group_of(int q, int G, const int* s_tiles) {
+    int lo = 0, hi = G;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (s_tiles[mid] <= q) lo = mid; else hi = mid;
+    }
+    return lo;
+}
+
 template <typename T, int OP, int BM, int BN, int WM, int WN, bool OUT32>
 __global__ void __launch_bounds__(WM * WN * 64)
 ragged_gemm_kernel(const RaggedParams p) {
@@ -107,29 +159,10 @@ ragged_gemm_kernel(const RaggedParams p) {
     const int wm = wave % WM, wn = wave / WM;
     const int G = p.groups;
 
-    // ---- segments: s_off[g] = the largest of offsets[0..g], clamped to [0, rows], so that
-    // no offsets, whatever they hold, lead outside the operands ----
-    if (wave == 0) {
-        const int per = (G + 1 + 63) / 64, g0 = lane * per;
-        int top = 0;
-        for (int i = 0; i < per; ++i)
-            if (g0 + i <= G) top = max(top, min(p.offsets[g0 + i], p.rows));
-        int before = top;
-        for (int d = 1; d < 64; d <<= 1) {
-            const int v = __shfl_up(before, d, 64);
-            if (lane >= d) before = max(before, v);
-        }
-        before = __shfl_up(before, 1, 64);
-        if (lane == 0) before = 0;
-        for (int i = 0; i < per; ++i)
-            if (g0 + i <= G) {
-                before = max(before, min(p.offsets[g0 + i], p.rows));
-                s_off[g0 + i] = before;
-            }
-    }
-    __syncthreads();
     int total;                         // (the host keeps its bound below 2^30)
     if constexpr (OP == kRaggedTN) {
+        if (wave == 0) read_segments(p, lane, s_off);
+        __syncthreads();
         total = G * p.tiles_i * p.tiles_j;
         // Tiles differ in length with their group: they are dealt out longest first, and every
         // other round backwards, so that the workgroups' sums come out nearly even.
@@ -145,22 +178,8 @@ ragged_gemm_kernel(const RaggedParams p) {
         __syncthreads();
     } else {
         if (wave == 0) {
-            const int per = (G + 63) / 64, g0 = lane * per;
-            int own = 0;
-            for (int i = 0; i < per; ++i)
-                if (g0 + i < G) own += (s_off[g0 + i + 1] - s_off[g0 + i] + BM - 1) / BM;
-            int incl = own;
-            for (int d = 1; d < 64; d <<= 1) {
-                const int v = __shfl_up(incl, d, 64);
-                if (lane >= d) incl += v;
-            }
-            int run = incl - own;
-            for (int i = 0; i < per; ++i)
-                if (g0 + i < G) {
-                    s_tiles[g0 + i] = run;
-                    run += (s_off[g0 + i + 1] - s_off[g0 + i] + BM - 1) / BM;
-                }
-            if (lane == 63) s_tiles[G] = incl;
+            read_segments(p, lane, s_off);
+            count_row_tiles<BM>(G, lane, s_off, s_tiles);
         }
         __syncthreads();
         total = __builtin_amdgcn_readfirstlane(s_tiles[G]) * p.tiles_j;
@@ -201,13 +220,7 @@ ragged_gemm_kernel(const RaggedParams p) {
             g = s_tiles[rank];
             band_order(L - rank * per, p.tiles_i, p.tiles_j, ti, tj);
         } else {
-            const int q = L / p.tiles_j;
-            int lo = 0, hi = G;             // the last g with s_tiles[g] <= q
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) >> 1;
-                if (s_tiles[mid] <= q) lo = mid; else hi = mid;
-            }
-            g = lo;
+            g = group_of(L / p.tiles_j, G, s_tiles);
             band_order(L - s_tiles[g] * p.tiles_j, max(s_tiles[g + 1] - s_tiles[g], 1), p.tiles_j, ti, tj);
         }
         t.g = __builtin_amdgcn_readfirstlane(g);
@@ -485,6 +498,104 @@ ragged_gemm_kernel(const RaggedParams p) {
     wait_vmem<0>();      // no copy into LDS outlives the workgroup
 }
 
+// The forward product for few rows a group (generation, down to a single token), bound by the
+// bytes of the weights and, in small calls, by latency.  A weight is used by at most 16 rows
+// of a tile, so nothing is gained by LDS: every wave loads fragments straight into registers,
+// AHEAD steps deep.  A workgroup's waves share a tile of 16 rows and 16 CT columns and split the
+// contraction (wave w takes the steps w, w + NW, ...), so that even a small layer spreads
+// over many CUs with all of its bytes in flight; their sums meet in LDS, added in the waves'
+// order.  Each tile starts its walk at another step, so that workgroups in step with
+// each other do not read the same few columns of rows that share memory channels (16 x 32
+// tiles, 8 x 4096 x 7168 in 8 groups: 113 -> 83 us).
+// 16 x 16 tiles with eight waves: one row of 4096 x 7168 13.4 us (16 x 32 with four: 18.8 us);
+// with 1024 tiles of 16 x 32 and more they are equal, and fewer waves cost less to join.
+template <typename T, int CT, int NW, int AHEAD, int PER_SIMD>
+__global__ void __launch_bounds__(NW * 64, PER_SIMD)
+ragged_few_rows_kernel(const RaggedParams p) {
+    __shared__ int s_off[kMaxRaggedGroups + 1], s_tiles[kMaxRaggedGroups + 1];
+    __shared__ v4f s_sum[NW][CT][64];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int l16 = lane & 15, lgrp = lane >> 4;
+    if (wave == 0) {
+        read_segments(p, lane, s_off);
+        count_row_tiles<16>(p.groups, lane, s_off, s_tiles);
+    }
+    __syncthreads();
+    const int total = __builtin_amdgcn_readfirstlane(s_tiles[p.groups]) * p.tiles_j;
+    int place = blockIdx.x;
+    if (gridDim.x % kXcdCount == 0) place = place % kXcdCount * (gridDim.x / kXcdCount) + place / kXcdCount;
+    // a lane's row, and its c of a step: 16 lgrp + 0 .. 15 (the order of c is free as long as
+    // both operands share it; this one makes a lane's two halves of a step adjacent)
+    const uint32_t p_lane = (uint32_t)(l16 * (int)p.ldp + lgrp * 16) * 2, q_lane = (uint32_t)(l16 * (int)p.ldq + lgrp * 16) * 2;
+    const int steps = (p.nc + kStep - 1) / kStep;
+    for (int L = place; L < total; L += gridDim.x) {
+        const int g = __builtin_amdgcn_readfirstlane(group_of(L / p.tiles_j, p.groups, s_tiles));
+        int ti, tj;
+        band_order(L - s_tiles[g] * p.tiles_j, s_tiles[g + 1] - s_tiles[g], p.tiles_j, ti, tj);
+        const int i0 = __builtin_amdgcn_readfirstlane(ti) * 16, j0 = __builtin_amdgcn_readfirstlane(tj) * 16 * CT;
+        const int seg0 = __builtin_amdgcn_readfirstlane(s_off[g]);
+        const int rows = min(__builtin_amdgcn_readfirstlane(s_off[g + 1]) - seg0 - i0, 16), cols = min(p.nj - j0, 16 * CT);
+        const __amdgpu_buffer_rsrc_t pr = buffer_over(p.p + (long)(seg0 + i0) * p.ldp, rows * (int)p.ldp * 2);
+        const __amdgpu_buffer_rsrc_t qr = buffer_over(p.q + (long)g * p.q_gstride + (long)j0 * p.ldq, cols * (int)p.ldq * 2);
+        v4i pf[AHEAD][2], qf[AHEAD][CT][2];
+        // step s of the walk (past the contraction's end every lane is outside: zeros)
+        const int start = (int)((uint32_t)L * 8u % (uint32_t)steps);
+        auto load = [&](int slot, int s) DG_DEV_INLINE {
+            s = s >= steps ? steps : s + start < steps ? s + start : s + start - steps;
+            const int left = p.nc - s * kStep;
+            const int soff = left > 0 ? s * kStep * 2 : 0;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const bool in = lgrp * 16 + h * 8 < left;
+                pf[slot][h] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(pr, in ? p_lane + h * 16 : kOutside, soff, 0));
+#pragma unroll
+                for (int t = 0; t < CT; ++t)
+                    qf[slot][t][h] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(
+                        qr, in ? q_lane + (uint32_t)(t * 16 * (int)p.ldq * 2) + h * 16 : kOutside, soff, 0));
+            }
+        };
+        v4f acc[CT];
+#pragma unroll
+        for (int t = 0; t < CT; ++t) acc[t] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) load(i, wave + i * NW);
+        for (int s = wave; s < steps; s += AHEAD * NW) {
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int t = 0; t < CT; ++t) acc[t] = T::mfma(qf[i][t][h], pf[i][h], acc[t]);
+                load(i, s + (AHEAD + i) * NW);
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < CT; ++t) s_sum[wave][t][lane] = acc[t];
+        __syncthreads();
+        if (tid < CT * 64) {
+            v4f sum = s_sum[0][wave][lane];
+#pragma unroll
+            for (int w = 1; w < NW; ++w) sum += s_sum[w][wave][lane];
+            const int col = wave * 16 + lgrp * 4;
+            if (l16 < rows && col < cols) {
+                uint2* at = (uint2*)((uint16_t*)p.d + (long)(seg0 + i0 + l16) * p.ldd + j0 + col);
+                *at = uint2{pack2<T>(sum[0], sum[1]), pack2<T>(sum[2], sum[3])};
+            }
+        }
+        __syncthreads();               // the sums are read before the next tile's are written
+    }
+}
+
+template <typename T, int CT, int NW, int AHEAD, int PER_SIMD>
+hipError_t launch_few_rows(const RaggedParams& p, int grid, hipStream_t stream) {
+    hipLaunchKernelGGL((ragged_few_rows_kernel<T, CT, NW, AHEAD, PER_SIMD>), dim3(grid), dim3(NW * 64), 0, stream, p);
+    return hipGetLastError();
+}
+template <typename T, int CT, int NW, int AHEAD, int PER_SIMD>
+hipError_t occupancy_few_rows(int* blocks) {
+    return hipOccupancyMaxActiveBlocksPerMultiprocessor(blocks, ragged_few_rows_kernel<T, CT, NW, AHEAD, PER_SIMD>, NW * 64, 0);
+}
+
 template <typename T, int OP, int BM, int BN, int WM, int WN, bool OUT32>
 hipError_t launch_ragged(const RaggedParams& p, int grid, hipStream_t stream) {
     hipLaunchKernelGGL((ragged_gemm_kernel<T, OP, BM, BN, WM, WN, OUT32>), dim3(grid), dim3(WM * WN * 64), 0, stream, p);
@@ -496,19 +607,39 @@ hipError_t occupancy_ragged(int* blocks) {
                                                         WM * WN * 64, 0);
 }
 
-// Relative times: 1024 256x256 tiles' worth of products take 4 (one workgroup a CU), with
-// 128x128 tiles (two a CU) 1/0.85 of it, from the forward pass of 32768 x 4096 x 7168 in
-// eight groups: 1647 us and 1929 us.  Few tiles: 64 x 4096 x 7168 in 16 groups 193 us and 156 us.
-#define DG_RAGGED_256(T, HALF, OP, OUT32)                                                  \
-    {OP, HALF, OUT32, 256, 256, 4.0, 4.0, &launch_ragged<T, OP, 256, 256, 2, 4, OUT32>,    \
+// The planner's figures (RaggedConfig), in us on the MI355X, from the products they stand beside:
+// round_time per step of a full round, alone_time per step of one tile with a CU to itself,
+// tile_time for a tile's beginning and end.
+//   256x256   32768 x 4096 x 7168, one group: 1420 TFLOP/s = 1.5 a step of 256 tiles; 16 tiles 1.3;
+//             weight gradients of two steps: 11 a round
+//   128x128   64 x 4096 x 7168, 16 groups: 155 us = 1.38 a step of 512 tiles (bound by bytes),
+//             1.04 where bound by products; 256 tiles 0.97
+//   32x128    512 tiles 174 us, 256 tiles 102 us; pays where 128x128 tiles would leave a
+//             second round nearly empty (48 groups of 15 rows, n 1408, k 2048: 75 us for 90 us)
+//   16x32     8 x 4096 x 7168, 8 groups: 83 us = 0.185 a step and tile of a CU (32x128 102 us),
+//             256 rows in 16 groups 260 us = 0.29
+//   16x16     the same 87 us = 0.097 and 318 us = 0.177; one row of 4096 x 7168: 13.4 us = 0.12 a
+//             step (16x32 18.9, 32x128 54 us)
+#define DG_RAGGED_256(T, HALF, OP, OUT32)                                                       \
+    {OP, HALF, OUT32, 256, 256, 1.5, 1.3, 7.5, 0.0, &launch_ragged<T, OP, 256, 256, 2, 4, OUT32>, \
      &occupancy_ragged<T, OP, 256, 256, 2, 4, OUT32>}
-#define DG_RAGGED_128(T, HALF, OP, OUT32)                                                  \
-    {OP, HALF, OUT32, 128, 128, 2.35, 1.4, &launch_ragged<T, OP, 128, 128, 2, 2, OUT32>,   \
+#define DG_RAGGED_128(T, HALF, OP, OUT32)                                                       \
+    {OP, HALF, OUT32, 128, 128, 1.2, 0.97, 3.4, 0.0, &launch_ragged<T, OP, 128, 128, 2, 2, OUT32>, \
      &occupancy_ragged<T, OP, 128, 128, 2, 2, OUT32>}
-#define DG_RAGGED_TYPE(T, HALF)                                                            \
-    DG_RAGGED_256(T, HALF, kRaggedNT, false), DG_RAGGED_128(T, HALF, kRaggedNT, false),    \
-    DG_RAGGED_256(T, HALF, kRaggedNN, false), DG_RAGGED_128(T, HALF, kRaggedNN, false),    \
-    DG_RAGGED_256(T, HALF, kRaggedTN, false), DG_RAGGED_128(T, HALF, kRaggedTN, false),    \
+#define DG_RAGGED_32(T, HALF, OP)                                                               \
+    {OP, HALF, 0, 32, 128, 1.9, 0.91, 2.0, 0.0, &launch_ragged<T, OP, 32, 128, 1, 4, false>,  \
+     &occupancy_ragged<T, OP, 32, 128, 1, 4, false>}
+#define DG_RAGGED_16(T, HALF)                                                                   \
+    {kRaggedNT, HALF, 0, 16, 32, 0.185, 0.168, 2.0, 0.0065, &launch_few_rows<T, 2, 4, 4, 3>,       \
+     &occupancy_few_rows<T, 2, 4, 4, 3>},                                                       \
+    {kRaggedNT, HALF, 0, 16, 16, 0.097, 0.12, 2.0, 0.005, &launch_few_rows<T, 1, 8, 3, 4>,       \
+     &occupancy_few_rows<T, 1, 8, 3, 4>}
+#define DG_RAGGED_TYPE(T, HALF)                                                                 \
+    DG_RAGGED_256(T, HALF, kRaggedNT, false), DG_RAGGED_128(T, HALF, kRaggedNT, false),         \
+    DG_RAGGED_32(T, HALF, kRaggedNT), DG_RAGGED_16(T, HALF),                                    \
+    DG_RAGGED_256(T, HALF, kRaggedNN, false), DG_RAGGED_128(T, HALF, kRaggedNN, false),         \
+    DG_RAGGED_32(T, HALF, kRaggedNN),                                                           \
+    DG_RAGGED_256(T, HALF, kRaggedTN, false), DG_RAGGED_128(T, HALF, kRaggedTN, false),         \
     DG_RAGGED_256(T, HALF, kRaggedTN, true), DG_RAGGED_128(T, HALF, kRaggedTN, true)
 
 const RaggedConfig kConfigs[] = {DG_RAGGED_TYPE(Bf16, 0), DG_RAGGED_TYPE(F16, 1)};

@@ -28,6 +28,25 @@ bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(
 
 long ceil_div(long a, long b) { return (a + b - 1) / b; }
 
+// CUs of the current device, whatever the cap (0: no usable device).
+int device_cus() {
+    static std::atomic<int> known[64];
+    int dev = 0, cus = 0;
+    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) {
+        (void)hipGetLastError();
+        return 0;
+    }
+    cus = known[dev].load(std::memory_order_relaxed);
+    if (cus == 0) {
+        if (hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || cus <= 0) {
+            (void)hipGetLastError();
+            return 0;
+        }
+        known[dev].store(cus, std::memory_order_relaxed);
+    }
+    return cus;
+}
+
 // Workgroups of config c that fit a CU (the same on every device the library runs on).
 int blocks_per_cu(const dg::RaggedConfig* c, int index) {
     static std::atomic<int> known[kMaxConfigs];
@@ -42,14 +61,31 @@ int blocks_per_cu(const dg::RaggedConfig* c, int index) {
     return v;
 }
 
-// Expected tiles of D, for the choice of a tile: a filled group wastes half a row tile on
-// average, and has one at least.
+// Expected tiles of D, for the choice of a tile.  The split of the rows over the groups is on the
+// device: with many rows a group wastes half a row tile on average, with few each group
+// has one, and the longer ones a few more.
 double tiles_expected(int op, const dg::RaggedParams& p, int bm, int bn) {
     const double columns = (double)ceil_div(p.nj, bn);
     if (op == dg::kRaggedTN) return (double)p.groups * ceil_div(p.ni, bm) * columns;
-    const double filled = p.groups < p.rows ? p.groups : p.rows;
-    const double split = (double)p.rows / bm + 0.5 * filled;
-    return (split > filled ? split : filled) * columns;
+    const double filled = p.groups < p.rows ? p.groups : p.rows, whole = (double)p.rows / bm;
+    return (whole >= filled ? whole + 0.5 * filled : filled + 0.25 * whole) * columns;
+}
+
+// Expected time (us) of a configuration with `slots` workgroups at a time on `cus` CUs.
+double time_expected(int op, const dg::RaggedParams& p, const dg::RaggedConfig& c, int cus, int slots) {
+    const double tiles = tiles_expected(op, p, c.bm, c.bn);
+    const double length = op == dg::kRaggedTN ? (double)p.rows / p.groups : p.nc;   // of the contraction
+    const double steps = std::ceil(length / 128) * 2;
+    if (c.row_time > 0) {      // bound by bytes: no rounds
+        const double filled = p.groups < p.rows ? p.groups : p.rows;
+        const double rows = p.rows / filled < c.bm ? p.rows / filled : c.bm;
+        const double step = (c.round_time + c.row_time * rows) * tiles / cus;
+        return (step > c.alone_time ? step : c.alone_time) * steps + c.tile_time;
+    }
+    double rounds = tiles / slots;
+    // part of a round takes a round's time (over many rounds it evens out)
+    if (rounds < 2) rounds = rounds <= 1.04 ? 1 : 2;
+    return (tiles <= cus ? c.alone_time : c.round_time * rounds) * steps + rounds * c.tile_time;
 }
 
 // Upper bound of the tiles of D: the rows' exact split over the groups is on the device.
@@ -62,9 +98,10 @@ long tiles_bound(int op, const dg::RaggedParams& p, int bm, int bn) {
 int launch_ragged(int op, int half, int out_f32, dg::RaggedParams& p, void* stream) {
     int count = 0;
     const dg::RaggedConfig* cfgs = dg::ragged_configs(&count);
-    const int units = dg_get_num_cus();
-    if (units < 0) return DG_ERR_HIP;
-    // the tile whose rounds over the CUs take least time (RaggedConfig::round_time)
+    const int cus = device_cus(), units = dg_get_num_cus();
+    if (cus <= 0 || units <= 0) return DG_ERR_HIP;
+    // The tile that is expected to take least time on the whole device: a cap of the CUs leaves
+    // the plan, and with it the order of the sums, as it is.
     int best = -1;
     double best_time = 0.0;
     for (int i = 0; i < count && i < kMaxConfigs; ++i) {
@@ -74,9 +111,7 @@ int launch_ragged(int op, int half, int out_f32, dg::RaggedParams& p, void* stre
             best = i;
             break;
         }
-        const double tiles = tiles_expected(op, p, c.bm, c.bn);
-        const double time = tiles <= units ? c.alone_time
-                                           : std::ceil(tiles / ((double)units * blocks_per_cu(&c, i))) * c.round_time;
+        const double time = time_expected(op, p, c, cus, cus * blocks_per_cu(&c, i));
         if (best < 0 || time < best_time) {
             best = i;
             best_time = time;

@@ -29,7 +29,7 @@ hipError_t two(int* blocks) {
     *blocks = 2;
     return hipSuccess;
 }
-#define ROW(OP, HALF, F32) {OP, HALF, F32, 128, 128, 1.0, 1.0, &record<OP, HALF, F32>, &two}
+#define ROW(OP, HALF, F32) {OP, HALF, F32, 128, 128, 1.0, 1.0, 1.0, 0.0, &record<OP, HALF, F32>, &two}
 const dg::RaggedConfig kRows[] = {ROW(0, 0, 0), ROW(1, 0, 0), ROW(2, 0, 0), ROW(2, 0, 1),
                                   ROW(0, 1, 0), ROW(1, 1, 0), ROW(2, 1, 0), ROW(2, 1, 1)};
 int g_failures = 0;
@@ -55,6 +55,14 @@ hipError_t launch_adamw(const AdamwParams& p, long chunks, hipStream_t) {
 
 extern "C" int dg_get_num_cus(void) { return g_cus; }
 extern "C" hipError_t hipGetLastError(void) { return hipSuccess; }
+extern "C" hipError_t hipGetDevice(int* device) {
+    *device = 0;
+    return hipSuccess;
+}
+extern "C" hipError_t hipDeviceGetAttribute(int* value, hipDeviceAttribute_t, int) {
+    *value = 256;
+    return hipSuccess;
+}
 
 int main() {
     void* const a = (void*)0x1000;
