@@ -90,13 +90,15 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.dg_transform_sa_mn_major.restype = I
     lib.dg_check_contiguous_layout.argtypes = [P, I, I, P]
     lib.dg_check_contiguous_layout.restype = I
-    lib.dg_m_grouped_gemm_ragged_nt.argtypes = [P, L, P, P, L, P, I, I, I, I, I, P]
+    lib.dg_m_grouped_gemm_ragged_nt.argtypes = [P, L, P, P, L, P, I, I, I, I, I, P, L, P]
     lib.dg_m_grouped_gemm_ragged_nt.restype = I
-    lib.dg_m_grouped_gemm_ragged_nn.argtypes = [P, L, P, P, L, P, I, I, I, I, I, P]
+    lib.dg_m_grouped_gemm_ragged_nn.argtypes = [P, L, P, P, L, P, I, I, I, I, I, P, L, P]
     lib.dg_m_grouped_gemm_ragged_nn.restype = I
-    lib.dg_k_grouped_gemm_ragged_tn.argtypes = [P, L, P, L, P, P, I, I, I, I, I, I, I, P]
+    lib.dg_k_grouped_gemm_ragged_tn.argtypes = [P, L, P, L, P, P, I, I, I, I, I, I, I, P, L, P]
     lib.dg_k_grouped_gemm_ragged_tn.restype = I
-    lib.dg_set_ragged_tile.argtypes = [I, I]
+    lib.dg_ragged_workspace_bytes.argtypes = [I, I, I, I, I, I, I]
+    lib.dg_ragged_workspace_bytes.restype = L
+    lib.dg_set_ragged_tile.argtypes = [I, I, I]
     lib.dg_set_ragged_tile.restype = I
     lib.dg_ragged_tile_info.argtypes = [I, P]
     lib.dg_ragged_tile_info.restype = I
@@ -422,7 +424,38 @@ def _raw_stream(stream):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _ragged_with_weights(call, a, b, d, offsets, transposed, stream):
+DG_RAGGED_NT, DG_RAGGED_NN, DG_RAGGED_TN = 0, 1, 2
+
+
+def dg_ragged_workspace_bytes(product, m_total, n, k, num_groups, dtype, d_dtype) -> int:
+    """Bytes of workspace that a ragged product (DG_RAGGED_*) of these sizes can use; types as
+    DG_DTYPE codes (0 float32, 1 bfloat16, 2 float16)."""
+    v = int((_lib or load_library()).dg_ragged_workspace_bytes(product, m_total, n, k, num_groups, dtype, d_dtype))
+    if v < 0:
+        raise DGError(v, "dg_ragged_workspace_bytes")
+    return v
+
+
+def _ragged_workspace(product, rows, n, k, groups, dtype, d_dtype, workspace, stream, device):
+    """(tensor to keep until the call is made, address, bytes) of the call's workspace: the one
+    given, or one from torch's allocator on the call's stream where the library wants any."""
+    import torch
+    if workspace is not None:
+        _dev(workspace, "workspace", (torch.uint8,), 1)
+        return workspace, workspace.data_ptr(), workspace.numel()
+    size = dg_ragged_workspace_bytes(product, rows, n, k, groups, dtype, d_dtype) if rows and n and k else 0
+    if size == 0:
+        return None, None, 0
+    if stream is None:
+        t = torch.empty(size, dtype=torch.uint8, device=device)
+    else:
+        s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))
+        with torch.cuda.stream(s):
+            t = torch.empty(size, dtype=torch.uint8, device=device)
+    return t, t.data_ptr(), size
+
+
+def _ragged_with_weights(call, a, b, d, offsets, transposed, workspace, stream):
     dt = _half_type((a, "a", 2), (b, "b", 3), (d, "d", 2))
     groups, n, k = b.shape
     rows, width = a.shape
@@ -432,25 +465,33 @@ def _ragged_with_weights(call, a, b, d, offsets, transposed, stream):
     if not b.is_contiguous():
         raise ValueError("b must be contiguous")
     lda, ldd = (a.stride(0), d.stride(0)) if rows > 1 else (wa, wd)
-    _check(getattr(_lib or load_library(), call)(a.data_ptr(), lda, b.data_ptr(), d.data_ptr(), ldd,
-                                                 _ragged_offsets(offsets, groups), rows, n, k, groups, dt,
-                                                 _raw_stream(stream)), call)
+    off = _ragged_offsets(offsets, groups)
+    kept, ws, size = None, None, 0
+    # (a product with a thousand tiles of 128 x 128 has no use for slices, nor has the forward one
+    # of a few rows, whose kernel divides the contraction by itself: no need to ask)
+    if workspace is not None or (rows * wd < 1 << 24 and (transposed or rows > 16)):
+        kept, ws, size = _ragged_workspace(DG_RAGGED_NN if transposed else DG_RAGGED_NT, rows, n, k, groups, dt, dt,
+                                           workspace, stream, a.device)
+    _check(getattr(_lib or load_library(), call)(a.data_ptr(), lda, b.data_ptr(), d.data_ptr(), ldd, off, rows, n, k,
+                                                 groups, dt, ws, size, _raw_stream(stream)), call)
 
 
-def dg_m_grouped_gemm_ragged_nt(a, b, d, offsets, stream=None) -> None:
+def dg_m_grouped_gemm_ragged_nt(a, b, d, offsets, stream=None, workspace=None) -> None:
     """Forward product grouped by expert: d[t] = a[t] . b[g]^T for the rows t of group g,
     which are offsets[g] .. offsets[g + 1] - 1 (int32, on the GPU; any lengths).  a [M, K],
-    b [G, N, K], d [M, N], all bfloat16 or all float16; rows outside every segment are left."""
-    _ragged_with_weights("dg_m_grouped_gemm_ragged_nt", a, b, d, offsets, False, stream)
+    b [G, N, K], d [M, N], all bfloat16 or all float16; rows outside every segment are left.
+    ``workspace`` (uint8, optional) is where the sums of a contraction cut into slices lie; without
+    one the call takes what it can use from torch's allocator."""
+    _ragged_with_weights("dg_m_grouped_gemm_ragged_nt", a, b, d, offsets, False, workspace, stream)
 
 
-def dg_m_grouped_gemm_ragged_nn(a, b, d, offsets, stream=None) -> None:
+def dg_m_grouped_gemm_ragged_nn(a, b, d, offsets, stream=None, workspace=None) -> None:
     """Gradient of the forward product's input: d[t] = a[t] . b[g], with a [M, N] the gradient
     of its output, b [G, N, K] its weights, d [M, K]."""
-    _ragged_with_weights("dg_m_grouped_gemm_ragged_nn", a, b, d, offsets, True, stream)
+    _ragged_with_weights("dg_m_grouped_gemm_ragged_nn", a, b, d, offsets, True, workspace, stream)
 
 
-def dg_k_grouped_gemm_ragged_tn(a, b, d, offsets, accumulate=False, stream=None) -> None:
+def dg_k_grouped_gemm_ragged_tn(a, b, d, offsets, accumulate=False, stream=None, workspace=None) -> None:
     """Gradient of the forward product's weights: d[g] = sum over the group's rows t of
     a[t]^T b[t], with a [M, N] the gradient of its output, b [M, K] its input, d [G, N, K] of
     their type or float32; ``accumulate`` adds to what d holds (otherwise a group without
@@ -464,9 +505,13 @@ def dg_k_grouped_gemm_ragged_tn(a, b, d, offsets, accumulate=False, stream=None)
     if not d.is_contiguous():
         raise ValueError("d must be contiguous")
     lda, ldb = (a.stride(0), b.stride(0)) if rows > 1 else (n, k)
+    off, d_dt = _ragged_offsets(offsets, groups), 0 if d.dtype == torch.float32 else dt
+    kept, ws, size = None, None, 0
+    if workspace is not None or groups * n * k < 1 << 24:
+        kept, ws, size = _ragged_workspace(DG_RAGGED_TN, rows, n, k, groups, dt, d_dt, workspace, stream, d.device)
     _check((_lib or load_library()).dg_k_grouped_gemm_ragged_tn(
-        a.data_ptr(), lda, b.data_ptr(), ldb, d.data_ptr(), _ragged_offsets(offsets, groups), rows, n, k, groups, dt,
-        0 if d.dtype == torch.float32 else dt, int(bool(accumulate)), _raw_stream(stream)), "dg_k_grouped_gemm_ragged_tn")
+        a.data_ptr(), lda, b.data_ptr(), ldb, d.data_ptr(), off, rows, n, k, groups, dt, d_dt, int(bool(accumulate)),
+        ws, size, _raw_stream(stream)), "dg_k_grouped_gemm_ragged_tn")
 
 
 # ---- training operators: an AdamW step over many tensors at once
@@ -654,9 +699,10 @@ def dg_set_kernel_config(config_id: int) -> None:
     _check(load_library().dg_set_kernel_config(int(config_id)), "dg_set_kernel_config")
 
 
-def dg_set_ragged_tile(block_m: int, block_n: int) -> None:
-    """Pin the tile of the calling thread's ragged products (0, 0: plan again)."""
-    _check(load_library().dg_set_ragged_tile(int(block_m), int(block_n)), "dg_set_ragged_tile")
+def dg_set_ragged_tile(block_m: int, block_n: int, slices: int = 0) -> None:
+    """Pin the tile of the calling thread's ragged products, and the slices of their contraction
+    (0, 0, 0: plan again)."""
+    _check(load_library().dg_set_ragged_tile(int(block_m), int(block_n), int(slices)), "dg_set_ragged_tile")
 
 
 def dg_ragged_tile_info() -> list:
@@ -712,6 +758,7 @@ __all__ = [
     "dg_quantize_fp8_128x128_fmt", "dg_get_aligned_ld_sa", "dg_transform_sa_mn_major",
     "dg_check_contiguous_layout", "dg_plan_tiles",
     "dg_m_grouped_gemm_ragged_nt", "dg_m_grouped_gemm_ragged_nn", "dg_k_grouped_gemm_ragged_tn",
+    "dg_ragged_workspace_bytes", "DG_RAGGED_NT", "DG_RAGGED_NN", "DG_RAGGED_TN",
     "AdamWPlan", "DG_STATE_F32", "DG_STATE_E4M3", "dg_adamw_plan_bytes", "dg_adamw_plan", "dg_adamw_step",
     "dg_set_kernel_config", "dg_kernel_config_info", "dg_describe_launch", "dg_set_ragged_tile", "dg_ragged_tile_info",
     "gemm_fp8_fp8_bf16_nt", "m_grouped_gemm_fp8_fp8_bf16_nt_contiguous", "m_grouped_gemm_fp8_fp8_bf16_nt_masked",

@@ -22,6 +22,7 @@
 //    from the offsets, which the host never reads.
 #include "dg_device.h"
 #include "dg_train.h"
+#include "../../include/dg.h"
 
 namespace dg {
 
@@ -147,6 +148,8 @@ ragged_gemm_kernel(const RaggedParams p) {
     static_assert(!PS || BM >= 128, "strided rows of whole 256-byte spans");
     static_assert(!QS || BN >= 128, "strided rows of whole 256-byte spans");
     static_assert(FN % 2 == 0, "the epilogue stores pairs of sub-tiles");
+    // kernels that can cut the contraction into slices (RaggedParams::slices): those for few tiles
+    constexpr bool SLICED = OUT32 && BM <= 128;
 
     // (each stage its own array, so that reads of one provably miss the copies into the other)
     __shared__ __attribute__((aligned(1024))) uint8_t smem0[STAGE];
@@ -196,7 +199,7 @@ ragged_gemm_kernel(const RaggedParams p) {
     // ---- a tile, all of it wave-uniform: group, first row and column of D (i0 from the segment's
     // first row seg0 in nt and nn), rows of the segment, contraction length ----
     struct Tile {
-        int g, i0, j0, seg0, seg_rows, nc;
+        int g, i0, j0, seg0, seg_rows, nc, slice;
         const uint16_t *pb, *qb;   // operands: the tile's first row (contiguous), or c = 0 at its
     };                             // first column (strided)
     // Steps of a tile: an even number and at least two.  Steps past the contraction's end (one
@@ -210,9 +213,12 @@ ragged_gemm_kernel(const RaggedParams p) {
     // the workgroup's next tile; past the last one a tile that copies nothing
     auto fetch_tile = [&](Tile& t) DG_DEV_INLINE -> bool {
         const int given = round * (int)gridDim.x + (OP == kRaggedTN && (round & 1) ? (int)gridDim.x - 1 - place : place);
-        const bool some = given < total;    // (total + grid fits an int)
-        const int L = some ? given : 0;
+        const bool some = given < total * (SLICED ? p.slices : 1);    // (that + grid fits an int)
+        int L = some ? given : 0;
         round += some;
+        // (slice by slice: the tiles of one share their operands' rows)
+        const int slice = SLICED ? L / max(total, 1) : 0;
+        L -= slice * total;
         int g, ti, tj;
         if constexpr (OP == kRaggedTN) {
             const int per = p.tiles_i * p.tiles_j;
@@ -229,9 +235,16 @@ ragged_gemm_kernel(const RaggedParams p) {
         t.seg0 = __builtin_amdgcn_readfirstlane(s_off[t.g]);
         t.seg_rows = __builtin_amdgcn_readfirstlane(s_off[t.g + 1]) - t.seg0;
         t.nc = some ? (OP == kRaggedTN ? t.seg_rows : p.nc) : 0;
-        t.pb = p.p + (PS ? (long)t.seg0 * p.ldp + t.i0 : (long)(t.seg0 + t.i0) * p.ldp);
-        t.qb = p.q + (OP == kRaggedTN ? (long)t.seg0 * p.ldq + t.j0
-                                      : (long)t.g * p.q_gstride + (QS ? (long)t.j0 : (long)t.j0 * p.ldq));
+        int c_first = 0;
+        if constexpr (SLICED) {
+            t.slice = __builtin_amdgcn_readfirstlane(slice);
+            const int part = (t.nc + p.slices * kStep - 1) / (p.slices * kStep) * kStep;
+            c_first = min(t.slice * part, t.nc);
+            t.nc = min(t.nc - c_first, part);
+        }
+        t.pb = p.p + (PS ? (long)(t.seg0 + c_first) * p.ldp + t.i0 : (long)(t.seg0 + t.i0) * p.ldp + c_first);
+        t.qb = p.q + (OP == kRaggedTN ? (long)(t.seg0 + c_first) * p.ldq + t.j0
+                                      : (long)t.g * p.q_gstride + (QS ? (long)c_first * p.ldq + t.j0 : (long)t.j0 * p.ldq + c_first));
         return some;
     };
 
@@ -389,7 +402,8 @@ ragged_gemm_kernel(const RaggedParams p) {
     typedef unsigned v4u __attribute__((ext_vector_type(4)));
     auto d_rows_of = [&](const Tile& t, bool some) DG_DEV_INLINE -> __amdgpu_buffer_rsrc_t {
         uint8_t* const base = (uint8_t*)p.d + (OP == kRaggedTN ? (long)t.g * p.d_gstride + (long)t.i0 * p.ldd
-                                                               : (long)(t.seg0 + t.i0) * p.ldd) * D_SIZE;
+                                                               : (long)(t.seg0 + t.i0) * p.ldd) * D_SIZE
+                              + (SLICED ? t.slice * p.slice_stride * 4 : 0);
         const int rows = min((OP == kRaggedTN ? p.ni : t.seg_rows) - t.i0, BM);
         return buffer_over(base, some ? rows * (int)p.ldd * D_SIZE : 0);
     };
@@ -596,6 +610,50 @@ hipError_t occupancy_few_rows(int* blocks) {
     return hipOccupancyMaxActiveBlocksPerMultiprocessor(blocks, ragged_few_rows_kernel<T, CT, NW, AHEAD, PER_SIMD>, NW * 64, 0);
 }
 
+// The join of a contraction cut into slices: four adjacent columns a thread, the slices' sums
+// added in their order (so a result does not depend on which workgroup came first).
+template <typename T, bool F32>
+__global__ void __launch_bounds__(256) ragged_join_kernel(const RaggedJoin p) {
+    __shared__ int s_rows[2];
+    if (p.offsets) {
+        if (threadIdx.x < 64) {
+            int top = 0;
+            for (int g = threadIdx.x; g <= p.groups; g += 64) top = max(top, p.offsets[g]);
+            for (int d = 32; d >= 1; d >>= 1) top = max(top, __shfl_xor(top, d, 64));
+            if (threadIdx.x == 0) {
+                s_rows[0] = max(p.offsets[0], 0);
+                s_rows[1] = top;
+            }
+        }
+        __syncthreads();
+    }
+    const int quads = p.width / 4;
+    for (long i = (long)blockIdx.x * 256 + threadIdx.x; i < p.rows * quads; i += (long)gridDim.x * 256) {
+        const long row = i / quads;
+        const int col = (int)(i - row * quads) * 4;
+        if (p.offsets && (row < s_rows[0] || row >= s_rows[1])) continue;
+        const float* at = p.sums + row * p.width + col;
+        v4f sum = *(const v4f*)at;
+        for (int k = 1; k < p.slices; ++k) sum += *(const v4f*)(at + k * p.slice_stride);
+        if constexpr (F32) {
+            v4f* d = (v4f*)((float*)p.d + row * p.ldd + col);
+            *d = p.accumulate ? *d + sum : sum;
+        } else {
+            uint2* d = (uint2*)((uint16_t*)p.d + row * p.ldd + col);
+            if (p.accumulate) {
+                float a, b;
+                unpack2<T>(d->x, a, b);
+                sum[0] += a;
+                sum[1] += b;
+                unpack2<T>(d->y, a, b);
+                sum[2] += a;
+                sum[3] += b;
+            }
+            *d = uint2{pack2<T>(sum[0], sum[1]), pack2<T>(sum[2], sum[3])};
+        }
+    }
+}
+
 template <typename T, int OP, int BM, int BN, int WM, int WN, bool OUT32>
 hipError_t launch_ragged(const RaggedParams& p, int grid, hipStream_t stream) {
     hipLaunchKernelGGL((ragged_gemm_kernel<T, OP, BM, BN, WM, WN, OUT32>), dim3(grid), dim3(WM * WN * 64), 0, stream, p);
@@ -621,24 +679,26 @@ hipError_t occupancy_ragged(int* blocks) {
 //   16x16     the same 87 us = 0.097 and 318 us = 0.177; one row of 4096 x 7168: 13.4 us = 0.12 a
 //             step (16x32 18.9, 32x128 54 us)
 #define DG_RAGGED_256(T, HALF, OP, OUT32)                                                       \
-    {OP, HALF, OUT32, 256, 256, 1.5, 1.3, 7.5, 0.0, &launch_ragged<T, OP, 256, 256, 2, 4, OUT32>, \
+    {OP, HALF, OUT32, 256, 256, 1.5, 1.3, 7.5, 0.0, 1, &launch_ragged<T, OP, 256, 256, 2, 4, OUT32>, \
      &occupancy_ragged<T, OP, 256, 256, 2, 4, OUT32>}
 #define DG_RAGGED_128(T, HALF, OP, OUT32)                                                       \
-    {OP, HALF, OUT32, 128, 128, 1.2, 0.97, 3.4, 0.0, &launch_ragged<T, OP, 128, 128, 2, 2, OUT32>, \
+    {OP, HALF, OUT32, 128, 128, 1.2, 0.97, 3.4, 0.0, OUT32 ? 32 : 1, &launch_ragged<T, OP, 128, 128, 2, 2, OUT32>, \
      &occupancy_ragged<T, OP, 128, 128, 2, 2, OUT32>}
-#define DG_RAGGED_32(T, HALF, OP)                                                               \
-    {OP, HALF, 0, 32, 128, 1.9, 0.91, 2.0, 0.0, &launch_ragged<T, OP, 32, 128, 1, 4, false>,  \
-     &occupancy_ragged<T, OP, 32, 128, 1, 4, false>}
+#define DG_RAGGED_32(T, HALF, OP, OUT32)                                                        \
+    {OP, HALF, OUT32, 32, 128, 1.9, 0.91, 2.0, 0.0, OUT32 ? 32 : 1, &launch_ragged<T, OP, 32, 128, 1, 4, OUT32>, \
+     &occupancy_ragged<T, OP, 32, 128, 1, 4, OUT32>}
 #define DG_RAGGED_16(T, HALF)                                                                   \
-    {kRaggedNT, HALF, 0, 16, 32, 0.185, 0.168, 2.0, 0.0065, &launch_few_rows<T, 2, 4, 4, 3>,       \
+    {kRaggedNT, HALF, 0, 16, 32, 0.185, 0.168, 2.0, 0.0065, 1, &launch_few_rows<T, 2, 4, 4, 3>, \
      &occupancy_few_rows<T, 2, 4, 4, 3>},                                                       \
-    {kRaggedNT, HALF, 0, 16, 16, 0.097, 0.12, 2.0, 0.005, &launch_few_rows<T, 1, 8, 3, 4>,       \
+    {kRaggedNT, HALF, 0, 16, 16, 0.097, 0.12, 2.0, 0.005, 1, &launch_few_rows<T, 1, 8, 3, 4>,   \
      &occupancy_few_rows<T, 1, 8, 3, 4>}
 #define DG_RAGGED_TYPE(T, HALF)                                                                 \
     DG_RAGGED_256(T, HALF, kRaggedNT, false), DG_RAGGED_128(T, HALF, kRaggedNT, false),         \
-    DG_RAGGED_32(T, HALF, kRaggedNT), DG_RAGGED_16(T, HALF),                                    \
+    DG_RAGGED_32(T, HALF, kRaggedNT, false), DG_RAGGED_16(T, HALF),                             \
+    DG_RAGGED_128(T, HALF, kRaggedNT, true), DG_RAGGED_32(T, HALF, kRaggedNT, true),            \
     DG_RAGGED_256(T, HALF, kRaggedNN, false), DG_RAGGED_128(T, HALF, kRaggedNN, false),         \
-    DG_RAGGED_32(T, HALF, kRaggedNN),                                                           \
+    DG_RAGGED_32(T, HALF, kRaggedNN, false),                                                    \
+    DG_RAGGED_128(T, HALF, kRaggedNN, true), DG_RAGGED_32(T, HALF, kRaggedNN, true),            \
     DG_RAGGED_256(T, HALF, kRaggedTN, false), DG_RAGGED_128(T, HALF, kRaggedTN, false),         \
     DG_RAGGED_256(T, HALF, kRaggedTN, true), DG_RAGGED_128(T, HALF, kRaggedTN, true)
 
@@ -649,6 +709,15 @@ const RaggedConfig kConfigs[] = {DG_RAGGED_TYPE(Bf16, 0), DG_RAGGED_TYPE(F16, 1)
 const RaggedConfig* ragged_configs(int* count) {
     *count = (int)(sizeof(kConfigs) / sizeof(kConfigs[0]));
     return kConfigs;
+}
+
+hipError_t launch_ragged_join(const RaggedJoin& p, hipStream_t stream) {
+    const long threads = p.rows * (p.width / 4), want = (threads + 255) / 256;
+    const dim3 grid((unsigned)(want < 4096 ? want : 4096));
+    if (p.out == DG_DTYPE_F32) hipLaunchKernelGGL((ragged_join_kernel<Bf16, true>), grid, dim3(256), 0, stream, p);
+    else if (p.out == DG_DTYPE_BF16) hipLaunchKernelGGL((ragged_join_kernel<Bf16, false>), grid, dim3(256), 0, stream, p);
+    else hipLaunchKernelGGL((ragged_join_kernel<F16, false>), grid, dim3(256), 0, stream, p);
+    return hipGetLastError();
 }
 
 }  // namespace dg

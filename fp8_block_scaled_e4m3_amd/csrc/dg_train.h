@@ -23,7 +23,27 @@ struct RaggedParams {
     int ni, nj, nc;          // extents of i, j, c (0 where it is the group's rows)
     int tiles_i, tiles_j;    // tn: exact; nt, nn: tiles_i unused
     int accumulate;          // tn: add to what D holds
+    int slices;              // > 1: the contraction is cut into as many parts, whose fp32 sums
+    long slice_stride;       // go to D + part * slice_stride (a workspace) and are joined later
 };
+
+// The join: D = [D +] the sum of the slices, in their order.  D is [rows][width] of the type
+// out (DG_DTYPE_*), a slice the same with rows of `width`; with `offsets` only the rows of
+// the segments are written.
+struct RaggedJoin {
+    const float* sums;
+    long slice_stride;
+    int slices;
+    void* d;
+    long ldd;
+    long rows;
+    int width;
+    int out;
+    int accumulate;
+    const int* offsets;
+    int groups;
+};
+hipError_t launch_ragged_join(const RaggedJoin& p, hipStream_t stream);
 
 constexpr int kMaxRaggedGroups = 1024;   // offsets are kept in LDS
 
@@ -37,6 +57,7 @@ struct RaggedConfig {
     // bytes of the weights and rows; a step then takes round_time + row_time per row for
     // every tile a CU has.
     double round_time, alone_time, tile_time, row_time;
+    int most_slices;         // parts that the contraction may be cut into (fp32 output only)
     hipError_t (*launch)(const RaggedParams&, int grid, hipStream_t);
     hipError_t (*occupancy)(int* blocks_per_cu);
 };

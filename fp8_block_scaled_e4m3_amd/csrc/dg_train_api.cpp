@@ -19,10 +19,11 @@ namespace {
 
 constexpr int kMaxConfigs = 64;
 constexpr long kMaxLd = 1l << 21;      // a tile is addressed with 31-bit offsets: 256 rows of ld fp32 values
+constexpr long kMaxWorkspace = 256l << 20;   // what dg_ragged_workspace_bytes asks for at most
 constexpr long kMaxTiles = 1l << 30;   // tile numbers, and one round past the last, are ints
 
 // dg_set_ragged_tile: 0 plans.  Per thread, like dg_set_kernel_config.
-thread_local int g_pinned_bm = 0, g_pinned_bn = 0;
+thread_local int g_pinned_bm = 0, g_pinned_bn = 0, g_pinned_slices = 0;
 
 bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
 
@@ -71,11 +72,16 @@ double tiles_expected(int op, const dg::RaggedParams& p, int bm, int bn) {
     return (whole >= filled ? whole + 0.5 * filled : filled + 0.25 * whole) * columns;
 }
 
-// Expected time (us) of a configuration with `slots` workgroups at a time on `cus` CUs.
-double time_expected(int op, const dg::RaggedParams& p, const dg::RaggedConfig& c, int cus, int slots) {
-    const double tiles = tiles_expected(op, p, c.bm, c.bn);
+long elements_of_d(int op, const dg::RaggedParams& p) {
+    return (op == dg::kRaggedTN ? (long)p.groups * p.ni : (long)p.rows) * p.nj;
+}
+
+// Expected time (us) of a configuration with `slots` workgroups at a time on `cus` CUs and the
+// contraction cut into `slices`.
+double time_expected(int op, const dg::RaggedParams& p, const dg::RaggedConfig& c, int cus, int slots, int slices) {
+    const double tiles = tiles_expected(op, p, c.bm, c.bn) * slices;
     const double length = op == dg::kRaggedTN ? (double)p.rows / p.groups : p.nc;   // of the contraction
-    const double steps = std::ceil(length / 128) * 2;
+    const double steps = std::ceil(length / (128 * slices)) * 2;
     if (c.row_time > 0) {      // bound by bytes: no rounds
         const double filled = p.groups < p.rows ? p.groups : p.rows;
         const double rows = p.rows / filled < c.bm ? p.rows / filled : c.bm;
@@ -85,7 +91,43 @@ double time_expected(int op, const dg::RaggedParams& p, const dg::RaggedConfig& 
     double rounds = tiles / slots;
     // part of a round takes a round's time (over many rounds it evens out)
     if (rounds < 2) rounds = rounds <= 1.04 ? 1 : 2;
-    return (tiles <= cus ? c.alone_time : c.round_time * rounds) * steps + rounds * c.tile_time;
+    const double time = (tiles <= cus ? c.alone_time : c.round_time * rounds) * steps + rounds * c.tile_time;
+    // the join: a launch, and the slices' sums written and read at about 4 TB/s
+    return slices == 1 ? time : time + 5.0 + 2.0 * 4.0 * slices * elements_of_d(op, p) / 4e6;
+}
+
+// The configuration and slices expected to take least time on the whole device (a cap of the
+// CUs leaves the plan, and with it the order of the sums, as it is); -1: none.  More than
+// one slice only where their sums fit the workspace.
+struct Plan {
+    int config = -1, slices = 1;
+};
+long slices_bytes(int op, const dg::RaggedParams& p, int slices) {
+    return slices == 1 ? 0 : slices * elements_of_d(op, p) * (long)sizeof(float);
+}
+Plan plan_ragged(int op, int half, int out_f32, const dg::RaggedParams& p, int cus, long workspace_bytes) {
+    int count = 0;
+    const dg::RaggedConfig* cfgs = dg::ragged_configs(&count);
+    Plan best;
+    double best_time = 0.0;
+    for (int i = 0; i < count && i < kMaxConfigs; ++i) {
+        const dg::RaggedConfig& c = cfgs[i];
+        if (c.op != op || c.half != half) continue;
+        const bool pinned = c.bm == g_pinned_bm && c.bn == g_pinned_bn;
+        if (pinned && c.out_f32 == out_f32 && g_pinned_slices <= 1) return Plan{i, 1};
+        if (pinned && c.most_slices > 1 && g_pinned_slices > 1 && slices_bytes(op, p, g_pinned_slices) <= workspace_bytes)
+            return Plan{i, g_pinned_slices};
+        const int slots = cus * blocks_per_cu(&c, i);
+        for (int slices = 1; slices <= c.most_slices; slices *= 2) {
+            if (slices == 1 ? c.out_f32 != out_f32 : slices_bytes(op, p, slices) > workspace_bytes) continue;
+            const double time = time_expected(op, p, c, cus, slots, slices);
+            if (best.config < 0 || time < best_time) {
+                best = Plan{i, slices};
+                best_time = time;
+            }
+        }
+    }
+    return best;
 }
 
 // Upper bound of the tiles of D: the rows' exact split over the groups is on the device.
@@ -95,54 +137,71 @@ long tiles_bound(int op, const dg::RaggedParams& p, int bm, int bn) {
     return (p.rows / bm + filled) * ceil_div(p.nj, bn);
 }
 
-int launch_ragged(int op, int half, int out_f32, dg::RaggedParams& p, void* stream) {
+int launch_ragged(int op, int half, int out_f32, dg::RaggedParams& p, void* workspace, long workspace_bytes,
+                  void* stream) {
     int count = 0;
     const dg::RaggedConfig* cfgs = dg::ragged_configs(&count);
     const int cus = device_cus(), units = dg_get_num_cus();
     if (cus <= 0 || units <= 0) return DG_ERR_HIP;
-    // The tile that is expected to take least time on the whole device: a cap of the CUs leaves
-    // the plan, and with it the order of the sums, as it is.
-    int best = -1;
-    double best_time = 0.0;
-    for (int i = 0; i < count && i < kMaxConfigs; ++i) {
-        const dg::RaggedConfig& c = cfgs[i];
-        if (c.op != op || c.half != half || c.out_f32 != out_f32) continue;
-        if (c.bm == g_pinned_bm && c.bn == g_pinned_bn) {
-            best = i;
-            break;
-        }
-        const double time = time_expected(op, p, c, cus, cus * blocks_per_cu(&c, i));
-        if (best < 0 || time < best_time) {
-            best = i;
-            best_time = time;
-        }
-    }
-    if (best < 0) return DG_ERR_UNSUPPORTED;
-    const dg::RaggedConfig& c = cfgs[best];
+    const Plan plan = plan_ragged(op, half, out_f32, p, cus, workspace ? workspace_bytes : 0);
+    if (plan.config < 0) return DG_ERR_UNSUPPORTED;
+    const dg::RaggedConfig& c = cfgs[plan.config];
     p.tiles_i = (int)ceil_div(p.ni, c.bm);
     p.tiles_j = (int)ceil_div(p.nj, c.bn);
-    long grid = (long)units * blocks_per_cu(&c, best);
+    long grid = (long)units * blocks_per_cu(&c, plan.config);
     const long tiles = tiles_bound(op, p, c.bm, c.bn);
-    if (tiles >= kMaxTiles) return DG_ERR_UNSUPPORTED;
-    if (tiles < grid) grid = tiles;
-    if (c.launch(p, (int)grid, static_cast<hipStream_t>(stream)) != hipSuccess) {
+    if (tiles >= kMaxTiles / plan.slices) return DG_ERR_UNSUPPORTED;
+    if (tiles * plan.slices < grid) grid = tiles * plan.slices;
+    p.slices = plan.slices;
+    dg::RaggedJoin join{};
+    if (plan.slices > 1) {
+        join.sums = static_cast<const float*>(workspace);
+        join.slice_stride = p.slice_stride = elements_of_d(op, p);
+        join.slices = plan.slices;
+        join.d = p.d;
+        join.ldd = p.ldd;
+        join.rows = op == dg::kRaggedTN ? (long)p.groups * p.ni : p.rows;
+        join.width = p.nj;
+        join.out = out_f32 ? DG_DTYPE_F32 : half ? DG_DTYPE_F16 : DG_DTYPE_BF16;
+        join.accumulate = p.accumulate;
+        join.offsets = op == dg::kRaggedTN ? nullptr : p.offsets;
+        join.groups = p.groups;
+        p.d = workspace;
+        p.ldd = p.nj;
+        p.accumulate = 0;
+    }
+    if (c.launch(p, (int)grid, static_cast<hipStream_t>(stream)) != hipSuccess ||
+        (plan.slices > 1 && dg::launch_ragged_join(join, static_cast<hipStream_t>(stream)) != hipSuccess)) {
         (void)hipGetLastError();
         return DG_ERR_HIP;
     }
     return DG_OK;
 }
 
+dg::RaggedParams params_of(int op, int m_total, int n, int k, int num_groups) {
+    dg::RaggedParams p{};
+    p.rows = m_total;
+    p.groups = num_groups;
+    p.ni = op == dg::kRaggedTN ? n : 0;
+    p.nj = op == dg::kRaggedNT ? n : k;
+    p.nc = op == dg::kRaggedNT ? k : op == dg::kRaggedNN ? n : 0;
+    return p;
+}
+
 // Checks shared by the three products: sizes, types, and each operand's row stride
 // (width_a, width_b, width_d elements wide).
 int check_ragged(const void* a, long lda, int width_a, const void* b, long ldb, int width_b, const void* d, long ldd,
-                 int width_d, const int* offsets, int m_total, int n, int k, int num_groups, int dtype) {
+                 int width_d, const int* offsets, int m_total, int n, int k, int num_groups, int dtype,
+                 const void* workspace, long workspace_bytes) {
+    if (workspace_bytes < 0 || (workspace_bytes > 0 && !workspace)) return DG_ERR_INVALID_ARG;
     if (m_total < 0 || n < 0 || k < 0 || num_groups < 1) return DG_ERR_INVALID_ARG;
     if (dtype != DG_DTYPE_BF16 && dtype != DG_DTYPE_F16) return DG_ERR_INVALID_ARG;
-    if (n % 8 || k % 8 || num_groups > dg::kMaxRaggedGroups) return DG_ERR_UNSUPPORTED;
+    if (n % 8 || k % 8 || num_groups > dg::kMaxRaggedGroups || m_total > 1 << 30) return DG_ERR_UNSUPPORTED;
     if (n == 0 || k == 0) return DG_OK;
     if (!d || !offsets || lda < width_a || ldb < width_b || ldd < width_d) return DG_ERR_INVALID_ARG;
     if (lda >= kMaxLd || ldb >= kMaxLd || ldd >= kMaxLd || n >= kMaxLd || k >= kMaxLd) return DG_ERR_UNSUPPORTED;
-    if (!aligned(a, 16) || !aligned(b, 16) || !aligned(d, 16) || lda % 8 || ldb % 8 || ldd % 8 || !aligned(offsets, 4))
+    if (!aligned(a, 16) || !aligned(b, 16) || !aligned(d, 16) || lda % 8 || ldb % 8 || ldd % 8 || !aligned(offsets, 4) ||
+        !aligned(workspace, 16))
         return DG_ERR_MISALIGNED;
     return DG_OK;
 }
@@ -201,23 +260,27 @@ int dg_ragged_tile_info(int index, int* out) {
     return DG_ERR_INVALID_ARG;
 }
 
-int dg_set_ragged_tile(int block_m, int block_n) {
+int dg_set_ragged_tile(int block_m, int block_n, int slices) {
     int tile[2] = {0, 0};
+    if (slices < 0 || slices > 32) return DG_ERR_INVALID_ARG;
     for (int i = 0; tile[0] != block_m || tile[1] != block_n; ++i)
         if (dg_ragged_tile_info(i, tile) != DG_OK) return DG_ERR_INVALID_ARG;
     g_pinned_bm = block_m;
     g_pinned_bn = block_n;
+    g_pinned_slices = slices;
     return DG_OK;
 }
 
 int dg_m_grouped_gemm_ragged_nt(const void* a, long lda, const void* b, void* d, long ldd, const int* offsets,
-                                int m_total, int n, int k, int num_groups, int dtype, void* stream) {
-    const int st = check_ragged(a, lda, k, b, k, k, d, ldd, n, offsets, m_total, n, k, num_groups, dtype);
+                                int m_total, int n, int k, int num_groups, int dtype, void* workspace,
+                                long workspace_bytes, void* stream) {
+    const int st = check_ragged(a, lda, k, b, k, k, d, ldd, n, offsets, m_total, n, k, num_groups, dtype, workspace,
+                                workspace_bytes);
     if (st != DG_OK) return st;
     if (m_total == 0 || n == 0) return DG_OK;
     if (k == 0) return DG_ERR_UNSUPPORTED;
     if (!a || !b) return DG_ERR_INVALID_ARG;
-    dg::RaggedParams p{};
+    dg::RaggedParams p = params_of(dg::kRaggedNT, m_total, n, k, num_groups);
     p.p = static_cast<const uint16_t*>(a);
     p.ldp = lda;
     p.q = static_cast<const uint16_t*>(b);
@@ -226,21 +289,19 @@ int dg_m_grouped_gemm_ragged_nt(const void* a, long lda, const void* b, void* d,
     p.d = d;
     p.ldd = ldd;
     p.offsets = offsets;
-    p.rows = m_total;
-    p.groups = num_groups;
-    p.nj = n;
-    p.nc = k;
-    return launch_ragged(dg::kRaggedNT, dtype == DG_DTYPE_F16, 0, p, stream);
+    return launch_ragged(dg::kRaggedNT, dtype == DG_DTYPE_F16, 0, p, workspace, workspace_bytes, stream);
 }
 
 int dg_m_grouped_gemm_ragged_nn(const void* a, long lda, const void* b, void* d, long ldd, const int* offsets,
-                                int m_total, int n, int k, int num_groups, int dtype, void* stream) {
-    const int st = check_ragged(a, lda, n, b, k, k, d, ldd, k, offsets, m_total, n, k, num_groups, dtype);
+                                int m_total, int n, int k, int num_groups, int dtype, void* workspace,
+                                long workspace_bytes, void* stream) {
+    const int st = check_ragged(a, lda, n, b, k, k, d, ldd, k, offsets, m_total, n, k, num_groups, dtype, workspace,
+                                workspace_bytes);
     if (st != DG_OK) return st;
     if (m_total == 0 || k == 0) return DG_OK;
     if (n == 0) return DG_ERR_UNSUPPORTED;
     if (!a || !b) return DG_ERR_INVALID_ARG;
-    dg::RaggedParams p{};
+    dg::RaggedParams p = params_of(dg::kRaggedNN, m_total, n, k, num_groups);
     p.p = static_cast<const uint16_t*>(a);
     p.ldp = lda;
     p.q = static_cast<const uint16_t*>(b);
@@ -249,24 +310,21 @@ int dg_m_grouped_gemm_ragged_nn(const void* a, long lda, const void* b, void* d,
     p.d = d;
     p.ldd = ldd;
     p.offsets = offsets;
-    p.rows = m_total;
-    p.groups = num_groups;
-    p.nj = k;
-    p.nc = n;
-    return launch_ragged(dg::kRaggedNN, dtype == DG_DTYPE_F16, 0, p, stream);
+    return launch_ragged(dg::kRaggedNN, dtype == DG_DTYPE_F16, 0, p, workspace, workspace_bytes, stream);
 }
 
 int dg_k_grouped_gemm_ragged_tn(const void* a, long lda, const void* b, long ldb, void* d, const int* offsets,
                                 int m_total, int n, int k, int num_groups, int dtype, int d_dtype, int accumulate,
-                                void* stream) {
-    const int st = check_ragged(a, lda, n, b, ldb, k, d, k, k, offsets, m_total, n, k, num_groups, dtype);
+                                void* workspace, long workspace_bytes, void* stream) {
+    const int st = check_ragged(a, lda, n, b, ldb, k, d, k, k, offsets, m_total, n, k, num_groups, dtype, workspace,
+                                workspace_bytes);
     if (st != DG_OK) return st;
     if (d_dtype != dtype && d_dtype != DG_DTYPE_F32) return DG_ERR_INVALID_ARG;
     if (accumulate != 0 && accumulate != 1) return DG_ERR_INVALID_ARG;
     if (n == 0 || k == 0) return DG_OK;
     if (m_total == 0 && accumulate) return DG_OK;
     if (m_total > 0 && (!a || !b)) return DG_ERR_INVALID_ARG;
-    dg::RaggedParams p{};
+    dg::RaggedParams p = params_of(dg::kRaggedTN, m_total, n, k, num_groups);
     p.p = static_cast<const uint16_t*>(a);
     p.ldp = lda;
     p.q = static_cast<const uint16_t*>(b);
@@ -275,12 +333,25 @@ int dg_k_grouped_gemm_ragged_tn(const void* a, long lda, const void* b, long ldb
     p.ldd = k;
     p.d_gstride = (long)n * k;
     p.offsets = offsets;
-    p.rows = m_total;
-    p.groups = num_groups;
-    p.ni = n;
-    p.nj = k;
     p.accumulate = accumulate;
-    return launch_ragged(dg::kRaggedTN, dtype == DG_DTYPE_F16, d_dtype == DG_DTYPE_F32, p, stream);
+    return launch_ragged(dg::kRaggedTN, dtype == DG_DTYPE_F16, d_dtype == DG_DTYPE_F32, p, workspace, workspace_bytes,
+                         stream);
+}
+
+long dg_ragged_workspace_bytes(int product, int m_total, int n, int k, int num_groups, int dtype, int d_dtype) {
+    if (product < DG_RAGGED_NT || product > DG_RAGGED_TN) return DG_ERR_INVALID_ARG;
+    const int op = product - DG_RAGGED_NT + dg::kRaggedNT;
+    // (any pointers and strides that pass: the sizes decide)
+    const int st = check_ragged(nullptr, k > n ? k : n, 0, nullptr, k > n ? k : n, 0, reinterpret_cast<void*>(16),
+                                k > n ? k : n, 0, reinterpret_cast<const int*>(16), m_total, n, k, num_groups, dtype,
+                                nullptr, 0);
+    if (st != DG_OK) return st;
+    if (d_dtype != dtype && !(op == dg::kRaggedTN && d_dtype == DG_DTYPE_F32)) return DG_ERR_INVALID_ARG;
+    if (m_total == 0 || n == 0 || k == 0) return 0;
+    const int cus = device_cus();
+    if (cus <= 0) return DG_ERR_HIP;
+    const dg::RaggedParams p = params_of(op, m_total, n, k, num_groups);
+    return slices_bytes(op, p, plan_ragged(op, dtype == DG_DTYPE_F16, d_dtype == DG_DTYPE_F32, p, cus, kMaxWorkspace).slices);
 }
 
 long dg_adamw_plan_bytes(const dg_adamw_tensor* tensors, int count) {

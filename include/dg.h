@@ -209,25 +209,30 @@ int dg_quantize_fp8_128x128_fmt(const void* x, int x_dtype, long ldx, int rows, 
  * an earlier one counts as that one, so no offsets lead outside the operands; rows of a
  * and d outside every segment (before the first, after the last) are not read and not
  * written.  A row that is NaN or infinite in one group's rows does not reach another's.
- * Requirements: n % 8 == 0, k % 8 == 0, num_groups <= 1024, n, k and leading dimensions
+ * Requirements: n % 8 == 0, k % 8 == 0, num_groups <= 1024, m_total <= 2^30, n, k and leading dimensions
  * below 2^21 and fewer than 2^30 tiles of d (else DG_ERR_UNSUPPORTED); a, b, d 16-byte aligned and leading dimensions
  * multiples of 8 (else DG_ERR_MISALIGNED); leading dimensions at least the width, non-null
  * pointers for non-empty problems (else DG_ERR_INVALID_ARG).  The contraction must not be
  * empty in the calls with weights (DG_ERR_UNSUPPORTED).  d must not overlap a or b.
  * dg_set_num_cus caps these kernels as it does the FP8 ones.
+ *   workspace  optional device memory (16-byte aligned) of the calling stream, of which nothing
+ *              is kept: where a product has few tiles and a long contraction, the
+ *              contraction is cut into slices, whose fp32 sums lie there until a second
+ *              kernel adds them up in order.  dg_ragged_workspace_bytes says how much
+ *              that takes; with less (or NULL, 0) the call is right, and slower.
  *
  * Forward: d[t][n] = sum_k a[t][k] b[g(t)][n][k].
  *   a [m_total][lda >= k]    d [m_total][ldd >= n] */
 int dg_m_grouped_gemm_ragged_nt(const void* a, long lda, const void* b, void* d, long ldd,
                                 const int* offsets, int m_total, int n, int k, int num_groups,
-                                int dtype, void* stream);
+                                int dtype, void* workspace, long workspace_bytes, void* stream);
 
 /* Gradient of the forward call's input, a being the gradient of its output:
  * d[t][k] = sum_n a[t][n] b[g(t)][n][k].
  *   a [m_total][lda >= n]    d [m_total][ldd >= k] */
 int dg_m_grouped_gemm_ragged_nn(const void* a, long lda, const void* b, void* d, long ldd,
                                 const int* offsets, int m_total, int n, int k, int num_groups,
-                                int dtype, void* stream);
+                                int dtype, void* workspace, long workspace_bytes, void* stream);
 
 /* Gradient of the forward call's weights, a being the gradient of its output and b its
  * input: d[g][n][k] = sum over g's rows t of a[t][n] b[t][k].
@@ -237,7 +242,14 @@ int dg_m_grouped_gemm_ragged_nn(const void* a, long lda, const void* b, void* d,
  *               0: they replace it, and a group without rows gets zeros. */
 int dg_k_grouped_gemm_ragged_tn(const void* a, long lda, const void* b, long ldb, void* d,
                                 const int* offsets, int m_total, int n, int k, int num_groups,
-                                int dtype, int d_dtype, int accumulate, void* stream);
+                                int dtype, int d_dtype, int accumulate,
+                                void* workspace, long workspace_bytes, void* stream);
+
+/* Bytes of workspace that a product of these sizes can use (0: none; a negative status for
+ * sizes that it refuses, or without a device). */
+enum { DG_RAGGED_NT = 0, DG_RAGGED_NN = 1, DG_RAGGED_TN = 2 };
+long dg_ragged_workspace_bytes(int product, int m_total, int n, int k, int num_groups, int dtype,
+                               int d_dtype);
 
 /* ---- Training operators: an AdamW step over many tensors at once ----
  *

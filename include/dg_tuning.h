@@ -41,11 +41,12 @@ int dg_kernel_config_info(int index, int* out);
 int dg_describe_launch(int layout, int m, int n, int k, int num_groups, int num_cus, int* out);
 
 /* Pin the tile of D that the calling thread's ragged products (dg_m_grouped_gemm_ragged_nt,
- * _nn, dg_k_grouped_gemm_ragged_tn) use, where the call has a kernel of that tile; 0, 0
- * plans again.  A tile that no call has gives DG_ERR_INVALID_ARG.  dg_ragged_tile_info fills
- * out[0..1] with block_m and block_n of the index-th tile, past the last one
- * DG_ERR_INVALID_ARG. */
-int dg_set_ragged_tile(int block_m, int block_n);
+ * _nn, dg_k_grouped_gemm_ragged_tn) use, where the call has a kernel of that tile, and the
+ * slices that the contraction is cut into (0 or 1: whole; more only where that kernel can and the
+ * workspace holds them); 0, 0, 0 plans again.  A tile that no call has, or more than 32
+ * slices, gives DG_ERR_INVALID_ARG.  dg_ragged_tile_info fills out[0..1] with block_m and
+ * block_n of the index-th tile, past the last one DG_ERR_INVALID_ARG. */
+int dg_set_ragged_tile(int block_m, int block_n, int slices);
 int dg_ragged_tile_info(int index, int* out);
 
 #ifdef __cplusplus

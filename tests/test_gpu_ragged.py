@@ -23,9 +23,12 @@ def gpu():
     dg.load_library()
 
 
-@pytest.fixture(autouse=True, params=[(0, 0)] + dg.dg_ragged_tile_info(), ids=lambda t: f"{t[0]}x{t[1]}")
+TILES = [(0, 0, 0)] + [(*t, 0) for t in dg.dg_ragged_tile_info()] + [(128, 128, 3), (32, 128, 4), (128, 128, 32)]
+
+
+@pytest.fixture(autouse=True, params=TILES, ids=lambda t: f"{t[0]}x{t[1]}by{t[2]}")
 def tile(request):
-    """Every test runs as planned and with each compiled tile."""
+    """Every test runs as planned, with each compiled tile, and with the contraction in slices."""
     dg.dg_set_ragged_tile(*request.param)
     yield request.param
     dg.dg_set_ragged_tile(0, 0)

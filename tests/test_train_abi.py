@@ -24,7 +24,7 @@ def lib():
 
 
 def weights_call(lib, name, **change):
-    args = dict(a=A, lda=128, b=B, d=D, ldd=128, offsets=OFF, m=10, n=64, k=128, g=4, dtype=BF16, stream=None)
+    args = dict(a=A, lda=128, b=B, d=D, ldd=128, offsets=OFF, m=10, n=64, k=128, g=4, dtype=BF16, workspace=None, bytes=0, stream=None)
     if name.endswith("nn"):
         args.update(lda=64, ldd=128)
     args.update(change)
@@ -43,7 +43,8 @@ WEIGHTS = ["dg_m_grouped_gemm_ragged_nt", "dg_m_grouped_gemm_ragged_nn"]
     (dict(lda=1 << 21), UNSUPPORTED), (dict(ldd=1 << 21), UNSUPPORTED), (dict(lda=1 << 40), UNSUPPORTED),
     (dict(a=A + 8), MISALIGNED), (dict(b=B + 2), MISALIGNED), (dict(d=D + 4), MISALIGNED), (dict(lda=132), MISALIGNED),
     (dict(ldd=1028), MISALIGNED), (dict(offsets=OFF + 2), MISALIGNED),
-    (dict(m=0), OK), (dict(m=0, a=None), OK)])
+    (dict(bytes=-1), INVALID), (dict(bytes=64), INVALID), (dict(workspace=0x50008, bytes=64), MISALIGNED),
+    (dict(m=(1 << 30) + 1), UNSUPPORTED), (dict(m=0), OK), (dict(m=0, a=None), OK)])
 def test_products_with_weights_refuse(lib, name, change, status):
     assert weights_call(lib, name, **change) == status
 
@@ -60,10 +61,11 @@ def test_empty_extents(lib):
     (dict(a=None), INVALID), (dict(b=None), INVALID), (dict(d=None), INVALID), (dict(offsets=None), INVALID),
     (dict(n=4), UNSUPPORTED), (dict(k=4), UNSUPPORTED), (dict(g=5000), UNSUPPORTED), (dict(ldb=1 << 21), UNSUPPORTED),
     (dict(a=A + 2), MISALIGNED), (dict(b=B + 8), MISALIGNED), (dict(d=D + 8), MISALIGNED), (dict(ldb=130), MISALIGNED),
+    (dict(bytes=-1), INVALID), (dict(bytes=64), INVALID), (dict(workspace=0x50004, bytes=64), MISALIGNED),
     (dict(n=0), OK), (dict(k=0), OK), (dict(m=0, accumulate=1), OK), (dict(m=0, accumulate=1, a=None, b=None), OK)])
 def test_weight_gradient_refuses(lib, change, status):
     args = dict(a=A, lda=64, b=B, ldb=128, d=D, offsets=OFF, m=10, n=64, k=128, g=4, dtype=BF16, d_dtype=BF16,
-                accumulate=0, stream=None)
+                accumulate=0, workspace=None, bytes=0, stream=None)
     args.update(change)
     assert lib.dg_k_grouped_gemm_ragged_tn(*args.values()) == status
 
@@ -71,10 +73,19 @@ def test_weight_gradient_refuses(lib, change, status):
 def test_ragged_tile_hooks(lib):
     tiles = dg.dg_ragged_tile_info()
     assert (128, 128) in tiles and (256, 256) in tiles and len(set(tiles)) == len(tiles)
-    for t in tiles + [(0, 0)]:
+    for t in tiles + [(128, 128, 4), (0, 0)]:
         dg.dg_set_ragged_tile(*t)
-    assert lib.dg_set_ragged_tile(17, 32) == INVALID and lib.dg_ragged_tile_info(0, None) == INVALID
+    assert lib.dg_set_ragged_tile(17, 32, 0) == INVALID and lib.dg_set_ragged_tile(128, 128, 33) == INVALID
+    assert lib.dg_set_ragged_tile(128, 128, -1) == INVALID and lib.dg_ragged_tile_info(0, None) == INVALID
     assert lib.dg_ragged_tile_info(-1, (ctypes.c_int * 2)()) == INVALID
+
+
+@pytest.mark.parametrize("args,status", [
+    ((3, 10, 64, 64, 1, BF16, BF16), INVALID), ((-1, 10, 64, 64, 1, BF16, BF16), INVALID), ((0, -1, 64, 64, 1, BF16, BF16), INVALID),
+    ((0, 10, 60, 64, 1, BF16, BF16), UNSUPPORTED), ((0, 10, 64, 64, 1, F32, F32), INVALID), ((0, 10, 64, 64, 1, BF16, F32), INVALID),
+    ((2, 10, 64, 64, 1, BF16, F16), INVALID), ((2, 0, 64, 64, 1, BF16, F32), 0), ((1, 10, 0, 64, 1, F16, F16), 0)])
+def test_workspace_bytes(lib, args, status):
+    assert lib.dg_ragged_workspace_bytes(*args) == status
 
 
 def tensor(**change):
