@@ -17,6 +17,15 @@
 // A workgroup takes one chunk of one tensor (the plan's table says which), a thread eight
 // consecutive elements, so that every access is 8 to 32 bytes per lane and a block of 128
 // is 16 lanes.  Each byte of the state moves once each way.
+//
+// Bound by bytes (MI355X): 117 M weights with BF16 copies, 32-bit states and fp32 gradients
+// 637 us (30 bytes an element, 5.5 TB/s; a plain copy of the same size reaches 4.9), 8-bit
+// states and BF16 gradients 363 us (16.1 bytes, 5.2 TB/s); 96 odd-sized tensors of 13.9 M
+// elements 54 us (4.2 TB/s, beginning and end of the launch showing); 48 tensors of
+// 64 to 8192 elements 5.4 us, the launch.  Without gain: loads or stores that bypass L2 (32-bit
+// states +5% and +1% time), chunks of 512 to 8192 elements (+-1%), approximate quotient and
+// root instead of the rounded ones (-3% with 8-bit states, not worth codes that depend on
+// them).
 #include "dg_cast_math.h"
 #include "dg_train.h"
 #include "../../include/dg.h"

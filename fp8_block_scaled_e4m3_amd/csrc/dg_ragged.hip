@@ -8,9 +8,9 @@
 //
 //  * V_MFMA_F32_16X16X32 with fp32 accumulation.  Q feeds the instruction's rows and P its
 //    columns, so that a lane's four results are four adjacent j of one row of D.
-//  * One K step holds 64 c of both operands in LDS, copied there directly from memory.
-//    A contiguous operand keeps rows of 128 bytes; a fragment is one 16-byte read per
-//    lane.  A strided one keeps rows of BM or BN elements; a fragment is two of gfx950's
+//  * One step holds 64 c of both operands in LDS, two steps at a time, copied there directly
+//    from memory.  A contiguous operand keeps rows of 128 bytes; a fragment is one 16-byte read
+//    per lane.  A strided one keeps rows of BM or BN elements; a fragment is two of gfx950's
 //    transposing 8-byte reads, each of which hands lane l of a 16-lane group the four c of
 //    column l.  Both are XOR-swizzled (16-byte chunks of a row; 32-byte units) so that the
 //    lanes of one read fall into distinct banks; the swizzle is in the copies' source
@@ -20,6 +20,19 @@
 //    the segment are not written.
 //  * A persistent grid walks the tiles; the segments' row tiles are counted on the device
 //    from the offsets, which the host never reads.
+//
+// What it costs (MI355X, BF16).  One group, 32768 x 4096 x 7168, 256x256 tiles: 1427 TFLOP/s
+// forward, 1393 input gradient, 1240 weight gradient (1.75 rounds of tiles, so 1417 while all
+// CUs work); a library product of these operands 1545, 1350 and 1176.  With zeros for operands
+// the same instructions reach 1611 to 1750 TFLOP/s: with real ones the clock gives way
+// first, so what is left is energy a product, not stalls.  What brought it there, from 785 for
+// the same shape in eight groups: 256x256 tiles with reads of one half of a step behind the
+// products of the other (1090), bands of tiles per XCD (1170; 1.7 of 3.0 GB fetched), reads and copies
+// dealt out between the products (1209), tiles that follow one another without a break
+// (1323).  Tried without gain: raised wave priority around the products (-1%), bands of 4 and 16
+// (-0.5%, -1%), stores of D that bypass L2 (-1.5%), copies in the first half of the rows
+// (-2%), reads spread over half or all of the rows (-0.5%), four waves of 128x128 with
+// accumulators in AGPRs (the compiler moves them through VGPRs in the loop).
 #include "dg_device.h"
 #include "dg_train.h"
 #include "../../include/dg.h"
