@@ -679,31 +679,33 @@ hipError_t occupancy_ragged(int* blocks) {
 }
 
 // The planner's figures (RaggedConfig), in us on the MI355X, from the products they stand beside:
-// round_time per step of a full round, alone_time per step of one tile with a CU to itself,
+// round_time per step of a full round, each_time of one tile a CU, single_time of a few tiles,
 // tile_time for a tile's beginning and end.
-//   256x256   32768 x 4096 x 7168, one group: 1420 TFLOP/s = 1.5 a step of 256 tiles; 16 tiles 1.3;
+//   256x256   32768 x 4096 x 7168, one group: 1427 TFLOP/s = 1.5 a step of 256 tiles; 16 tiles 1.07;
 //             weight gradients of two steps: 11 a round
 //   128x128   64 x 4096 x 7168, 16 groups: 155 us = 1.38 a step of 512 tiles (bound by bytes),
-//             1.04 where bound by products; 256 tiles 0.97
-//   32x128    512 tiles 174 us, 256 tiles 102 us; pays where 128x128 tiles would leave a
-//             second round nearly empty (48 groups of 15 rows, n 1408, k 2048: 75 us for 90 us)
+//             1.04 where bound by products; 256 tiles 0.97; 8 tiles of 16 steps 10.5 in all; weight
+//             gradient of 60 tiles 0.72
+//   32x128    512 tiles 174 us, 256 tiles 102 us, 32 tiles 54 us; pays where 128x128 tiles would
+//             leave a second round nearly empty (48 groups of 15 rows, n 1408, k 2048: 75 us
+//             for 90 us)
 //   16x32     8 x 4096 x 7168, 8 groups: 83 us = 0.185 a step and tile of a CU (32x128 102 us),
 //             256 rows in 16 groups 260 us = 0.29
 //   16x16     the same 87 us = 0.097 and 318 us = 0.177; one row of 4096 x 7168: 13.4 us = 0.12 a
 //             step (16x32 18.9, 32x128 54 us)
 #define DG_RAGGED_256(T, HALF, OP, OUT32)                                                       \
-    {OP, HALF, OUT32, 256, 256, 1.5, 1.3, 7.5, 0.0, 1, &launch_ragged<T, OP, 256, 256, 2, 4, OUT32>, \
+    {OP, HALF, OUT32, 256, 256, 1.5, 1.5, 1.05, 7.5, 0.0, 1, &launch_ragged<T, OP, 256, 256, 2, 4, OUT32>, \
      &occupancy_ragged<T, OP, 256, 256, 2, 4, OUT32>}
 #define DG_RAGGED_128(T, HALF, OP, OUT32)                                                       \
-    {OP, HALF, OUT32, 128, 128, 1.2, 0.97, 3.4, 0.0, OUT32 ? 32 : 1, &launch_ragged<T, OP, 128, 128, 2, 2, OUT32>, \
+    {OP, HALF, OUT32, 128, 128, 1.2, OP == kRaggedTN ? 1.0 : 0.97, OP == kRaggedTN ? 0.72 : 0.42, 3.4, 0.0, OUT32 ? 32 : 1, &launch_ragged<T, OP, 128, 128, 2, 2, OUT32>, \
      &occupancy_ragged<T, OP, 128, 128, 2, 2, OUT32>}
 #define DG_RAGGED_32(T, HALF, OP, OUT32)                                                        \
-    {OP, HALF, OUT32, 32, 128, 1.9, 0.91, 2.0, 0.0, OUT32 ? 32 : 1, &launch_ragged<T, OP, 32, 128, 1, 4, OUT32>, \
+    {OP, HALF, OUT32, 32, 128, 1.9, 0.91, 0.42, 2.0, 0.0, OUT32 ? 32 : 1, &launch_ragged<T, OP, 32, 128, 1, 4, OUT32>, \
      &occupancy_ragged<T, OP, 32, 128, 1, 4, OUT32>}
 #define DG_RAGGED_16(T, HALF)                                                                   \
-    {kRaggedNT, HALF, 0, 16, 32, 0.185, 0.168, 2.0, 0.0065, 1, &launch_few_rows<T, 2, 4, 4, 3>, \
+    {kRaggedNT, HALF, 0, 16, 32, 0.185, 0.0, 0.168, 2.0, 0.0065, 1, &launch_few_rows<T, 2, 4, 4, 3>, \
      &occupancy_few_rows<T, 2, 4, 4, 3>},                                                       \
-    {kRaggedNT, HALF, 0, 16, 16, 0.097, 0.12, 2.0, 0.005, 1, &launch_few_rows<T, 1, 8, 3, 4>,   \
+    {kRaggedNT, HALF, 0, 16, 16, 0.097, 0.0, 0.12, 2.0, 0.005, 1, &launch_few_rows<T, 1, 8, 3, 4>,   \
      &occupancy_few_rows<T, 1, 8, 3, 4>}
 #define DG_RAGGED_TYPE(T, HALF)                                                                 \
     DG_RAGGED_256(T, HALF, kRaggedNT, false), DG_RAGGED_128(T, HALF, kRaggedNT, false),         \

@@ -52,11 +52,11 @@ struct RaggedConfig {
     int half;                // 0: BF16 operands, 1: FP16
     int out_f32;             // D in fp32 (else in the operands' type)
     int bm, bn;              // tile of D
-    // For the choice of a tile, in us: a step of c of a round of tiles that fills the CUs, of
-    // tiles with a CU each, and the beginning and end of a tile.  row_time > 0: bound by the
-    // bytes of the weights and rows; a step then takes round_time + row_time per row for
-    // every tile a CU has.
-    double round_time, alone_time, tile_time, row_time;
+    // For the choice of a tile, in us: a step of 64 c of a round of tiles that fills the CUs, of
+    // a tile on each CU, and of a single tile; the beginning and end of a tile.  row_time > 0:
+    // bound by the bytes of the weights and rows; a step then takes round_time + row_time per
+    // row for every tile a CU has, single_time at least.
+    double round_time, each_time, single_time, tile_time, row_time;
     int most_slices;         // parts that the contraction may be cut into (fp32 output only)
     hipError_t (*launch)(const RaggedParams&, int grid, hipStream_t);
     hipError_t (*occupancy)(int* blocks_per_cu);

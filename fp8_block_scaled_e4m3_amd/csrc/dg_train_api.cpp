@@ -86,14 +86,15 @@ double time_expected(int op, const dg::RaggedParams& p, const dg::RaggedConfig& 
         const double filled = p.groups < p.rows ? p.groups : p.rows;
         const double rows = p.rows / filled < c.bm ? p.rows / filled : c.bm;
         const double step = (c.round_time + c.row_time * rows) * tiles / cus;
-        return (step > c.alone_time ? step : c.alone_time) * steps + c.tile_time;
+        return (step > c.single_time ? step : c.single_time) * steps + c.tile_time;
     }
     double rounds = tiles / slots;
     // part of a round takes a round's time (over many rounds it evens out)
     if (rounds < 2) rounds = rounds <= 1.04 ? 1 : 2;
-    const double time = (tiles <= cus ? c.alone_time : c.round_time * rounds) * steps + rounds * c.tile_time;
-    // the join: a launch, and the slices' sums written and read at about 4 TB/s
-    return slices == 1 ? time : time + 5.0 + 2.0 * 4.0 * slices * elements_of_d(op, p) / 4e6;
+    const double step = tiles <= cus ? c.single_time + (c.each_time - c.single_time) * tiles / cus : c.round_time * rounds;
+    const double time = step * steps + rounds * c.tile_time;
+    // the join: a launch and its share of the call, the sums written and read at about 4 TB/s
+    return slices == 1 ? time : time + 9.0 + 2.0 * 4.0 * slices * elements_of_d(op, p) / 4e6;
 }
 
 // The configuration and slices expected to take least time on the whole device (a cap of the
@@ -120,6 +121,8 @@ Plan plan_ragged(int op, int half, int out_f32, const dg::RaggedParams& p, int c
         const int slots = cus * blocks_per_cu(&c, i);
         for (int slices = 1; slices <= c.most_slices; slices *= 2) {
             if (slices == 1 ? c.out_f32 != out_f32 : slices_bytes(op, p, slices) > workspace_bytes) continue;
+            // (slices are for CUs without a tile: all of them in one round)
+            if (slices > 1 && tiles_expected(op, p, c.bm, c.bn) * slices > slots) break;
             const double time = time_expected(op, p, c, cus, slots, slices);
             if (best.config < 0 || time < best_time) {
                 best = Plan{i, slices};

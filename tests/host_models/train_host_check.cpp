@@ -31,7 +31,7 @@ hipError_t two(int* blocks) {
     *blocks = 2;
     return hipSuccess;
 }
-#define ROW(OP, HALF, F32) {OP, HALF, F32, 128, 128, 1.0, 1.0, 1.0, 0.0, F32 ? 32 : 1, &record<OP, HALF, F32>, &two}
+#define ROW(OP, HALF, F32) {OP, HALF, F32, 128, 128, 1.0, 1.0, 1.0, 1.0, 0.0, F32 ? 32 : 1, &record<OP, HALF, F32>, &two}
 const dg::RaggedConfig kRows[] = {ROW(0, 0, 0), ROW(1, 0, 0), ROW(2, 0, 0), ROW(2, 0, 1),
                                   ROW(0, 1, 0), ROW(1, 1, 0), ROW(2, 1, 0), ROW(2, 1, 1)};
 int g_failures = 0;
