@@ -1,4 +1,5 @@
-"""Python binding of libdg.so: fine-grained-scaled FP8 E4M3 NT GEMM for MI355X.
+"""Python binding of libdg.so: fine-grained-scaled FP8 E4M3 NT GEMM for MI355X, and the operators that
+train experts for it (16-bit products with ragged segments and their gradients, AdamW).
 
 Argument marshalling only.  Each function has the name of the C entry point it
 calls (see ``include/dg.h`` for the operation, layouts and error behaviour),
