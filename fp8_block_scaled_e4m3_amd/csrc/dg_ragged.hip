@@ -21,18 +21,21 @@
 //  * A persistent grid walks the tiles; the segments' row tiles are counted on the device
 //    from the offsets, which the host never reads.
 //
-// What it costs (MI355X, BF16).  One group, 32768 x 4096 x 7168, 256x256 tiles: 1427 TFLOP/s
-// forward, 1393 input gradient, 1240 weight gradient (1.75 rounds of tiles, so 1417 while all
-// CUs work); a library product of these operands 1545, 1350 and 1176.  With zeros for operands
-// the same instructions reach 1611 to 1750 TFLOP/s: with real ones the clock gives way
-// first, so what is left is energy a product, not stalls.  What brought it there, from 785 for
+// What it costs (MI355X, BF16).  One group, 32768 x 4096 x 7168, 256x256 tiles, on two cards:
+// 1350 and 1430 TFLOP/s forward, 1289 and 1387 input gradient, 1148 and 1270 weight gradient
+// (1.75 rounds of tiles, so 1451 while all CUs work); a library product of these operands on the
+// same two 1481 and 1601, 1296 and 1393, 1107 and 1207.  With zeros for operands the forward
+// instructions reach 1600 (the library's 1900): real ones make the clock give way, and a part
+// of the rest is waits (27% of the waves' cycles).  What brought it there, from 785 for
 // the same shape in eight groups: 256x256 tiles with reads of one half of a step behind the
 // products of the other (1090), bands of tiles per XCD (1170; 1.7 of 3.0 GB fetched), reads and copies
 // dealt out between the products (1209), tiles that follow one another without a break
 // (1323).  Tried without gain: raised wave priority around the products (-1%), bands of 4 and 16
 // (-0.5%, -1%), stores of D that bypass L2 (-1.5%), copies in the first half of the rows
 // (-2%), reads spread over half or all of the rows (-0.5%), four waves of 128x128 with
-// accumulators in AGPRs (the compiler moves them through VGPRs in the loop).
+// accumulators in AGPRs (the compiler moves them through VGPRs in the loop), a ring of four
+// stages of 32 c (-12%, input gradient -7%, weight gradient -4%: a barrier costs 4% of 64 c, and
+// the copies' latency is covered already).
 #include "dg_device.h"
 #include "dg_train.h"
 #include "../../include/dg.h"

@@ -23,19 +23,20 @@
  * whose fp32 sums are added at the end; the result then agrees with the one-chain
  * result to fp32 rounding but need not be bit-identical to it.
  *
- * Conventions for every entry point:
+ * Conventions for every entry point (the training operators, at the end, state their own
+ * requirements and limits):
  *  - Pointers named a, sa, b, sb, d, m_indices, masked_m are DEVICE pointers owned by
  *    the caller.  The library never allocates, frees, synchronises or reads device
  *    memory on the host, so every call is asynchronous on `stream` and may be
  *    captured into a hipGraph.  `stream` is a hipStream_t (NULL = default stream).
  *  - The return value reports host-side validation and launch errors only
  *    (DG_OK on success).  Nothing is launched when validation fails.
- *  - Requirements checked on the host: non-null pointers for non-empty problems;
+ *  - Requirements of the FP8 products, checked on the host: non-null pointers for non-empty problems;
  *    K > 0 and K % 128 == 0 (else DG_ERR_UNSUPPORTED); N % 16 == 0 (else
  *    DG_ERR_UNSUPPORTED); a, b, d, sa, sb 16-byte aligned; lda, ldb multiples of 16
  *    and >= K; ldd a multiple of 8 and >= N; ld_sa a multiple of 4 and >= the row
  *    count (else DG_ERR_MISALIGNED / DG_ERR_INVALID_ARG).
- *  - Size limits (else DG_ERR_UNSUPPORTED): 256 * lda + K and 256 * ldb + K below
+ *  - Their size limits (else DG_ERR_UNSUPPORTED): 256 * lda + K and 256 * ldb + K below
  *    2^32 bytes, (K / 128) * ld_sa * 4 + 4096 below 2^32 bytes (for the grouped
  *    layouts lda = ldb = K), M * ldd * 4 below 2^63, and fewer than 2^30 output tiles;
  *    the kernels address each tile's operands through 32-bit offsets from the tile's
