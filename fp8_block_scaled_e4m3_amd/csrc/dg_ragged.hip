@@ -119,14 +119,14 @@ __device__ __forceinline__ void read_segments(const RaggedParams& p, int lane, i
         }
 }
 
-// The same wave: row tiles of the groups before each, s_tiles[groups] being all of them.
-template <int BM>
-__device__ __forceinline__ void count_row_tiles(int G, int lane, const int* s_off, int* s_tiles) {
+// The same wave: row tiles of `height` rows of the groups before each, s_tiles[groups] being all of them.
+__device__ __forceinline__ void count_row_tiles(int height, int G, int lane, const int* s_off, int* s_tiles) {
+    const int shift = 31 - __builtin_clz(height);    // (a power of two)
     const int per = (G + 63) / 64, g0 = lane * per;
     asm volatile("" ::: "memory");      // (one wave's LDS accesses complete in order)
     int own = 0;
     for (int i = 0; i < per; ++i)
-        if (g0 + i < G) own += (s_off[g0 + i + 1] - s_off[g0 + i] + BM - 1) / BM;
+        if (g0 + i < G) own += (s_off[g0 + i + 1] - s_off[g0 + i] + height - 1) >> shift;
     int incl = own;
     for (int d = 1; d < 64; d <<= 1) {
         const int v = __shfl_up(incl, d, 64);
@@ -136,7 +136,7 @@ __device__ __forceinline__ void count_row_tiles(int G, int lane, const int* s_of
     for (int i = 0; i < per; ++i)
         if (g0 + i < G) {
             s_tiles[g0 + i] = run;
-            run += (s_off[g0 + i + 1] - s_off[g0 + i] + BM - 1) / BM;
+            run += (s_off[g0 + i + 1] - s_off[g0 + i] + height - 1) >> shift;
         }
     if (lane == 63) s_tiles[G] = incl;
 }
@@ -166,6 +166,8 @@ ragged_gemm_kernel(const RaggedParams p) {
     static_assert(FN % 2 == 0, "the epilogue stores pairs of sub-tiles");
     // kernels that can cut the contraction into slices (RaggedParams::slices): those for few tiles
     constexpr bool SLICED = OUT32 && BM <= 128;
+    // the kernels that share a product (RaggedParams::cut)
+    constexpr bool CUT = OP != kRaggedTN && BM == 256, REST = OP != kRaggedTN && !OUT32 && BM == 128;
 
     // (each stage its own array, so that reads of one provably miss the copies into the other)
     __shared__ __attribute__((aligned(1024))) uint8_t smem0[STAGE];
@@ -198,10 +200,21 @@ ragged_gemm_kernel(const RaggedParams p) {
     } else {
         if (wave == 0) {
             read_segments(p, lane, s_off);
-            count_row_tiles<BM>(G, lane, s_off, s_tiles);
+            count_row_tiles(REST && p.cut ? 2 * BM : BM, G, lane, s_off, s_tiles);
         }
         __syncthreads();
         total = __builtin_amdgcn_readfirstlane(s_tiles[G]) * p.tiles_j;
+    }
+    int rest_first = 0;                // REST: the first tile left out by the 256x256 kernel
+    if constexpr (CUT || REST) {
+        if (p.cut) {
+            const int rest = total % p.cut;
+            // (half a round: two quadrants a CU, as many as are resident; with 0.6 of a round the
+            // second launch loses 1 to 3%, with half it wins 10 to 16%)
+            const int left_out = rest <= p.cut / 2 ? rest : 0;
+            rest_first = total - left_out;
+            total = CUT ? rest_first : left_out * 4;
+        }
     }
 
     // ---- a lane's place in its copies.  A copy is 1 KiB of a stage: 8 rows of 128 bytes
@@ -224,7 +237,12 @@ ragged_gemm_kernel(const RaggedParams p) {
     auto steps_of = [&](const Tile& t) DG_DEV_INLINE { return max((t.nc + 2 * kStep - 1) / (2 * kStep), 1) * 2; };
     int round = 0, place = blockIdx.x;      // place of the workgroup in a round
     // (neighbouring tiles to the workgroups of one XCD: they share its L2)
-    if (gridDim.x % kXcdCount == 0) place = place % kXcdCount * (gridDim.x / kXcdCount) + place / kXcdCount;
+    if (gridDim.x % kXcdCount == 0) {
+        // (quadrants: few, and only the device knows how many; dealt to the first workgroups, so
+        // that every XCD has its share)
+        const int dealt = REST && p.cut ? min((int)gridDim.x, (total + kXcdCount - 1) / kXcdCount * kXcdCount) : (int)gridDim.x;
+        if (place < dealt) place = place % kXcdCount * (dealt / kXcdCount) + place / kXcdCount;
+    }
     constexpr int D_SIZE = OUT32 ? 4 : 2;
     // the workgroup's next tile; past the last one a tile that copies nothing
     auto fetch_tile = [&](Tile& t) DG_DEV_INLINE -> bool {
@@ -235,6 +253,9 @@ ragged_gemm_kernel(const RaggedParams p) {
         // (slice by slice: the tiles of one share their operands' rows)
         const int slice = SLICED ? L / max(total, 1) : 0;
         L -= slice * total;
+        const int quadrant = L & 3;
+        if constexpr (REST)
+            if (p.cut) L = min(rest_first + (L >> 2), max(rest_first + (total >> 2) - 1, 0));
         int g, ti, tj;
         if constexpr (OP == kRaggedTN) {
             const int per = p.tiles_i * p.tiles_j;
@@ -244,6 +265,11 @@ ragged_gemm_kernel(const RaggedParams p) {
         } else {
             g = group_of(L / p.tiles_j, G, s_tiles);
             band_order(L - s_tiles[g] * p.tiles_j, max(s_tiles[g + 1] - s_tiles[g], 1), p.tiles_j, ti, tj);
+            if constexpr (REST)
+                if (p.cut) {
+                    ti = ti * 2 + (quadrant >> 1);
+                    tj = tj * 2 + (quadrant & 1);
+                }
         }
         t.g = __builtin_amdgcn_readfirstlane(g);
         t.i0 = __builtin_amdgcn_readfirstlane(ti) * BM;
@@ -251,6 +277,8 @@ ragged_gemm_kernel(const RaggedParams p) {
         t.seg0 = __builtin_amdgcn_readfirstlane(s_off[t.g]);
         t.seg_rows = __builtin_amdgcn_readfirstlane(s_off[t.g + 1]) - t.seg0;
         t.nc = some ? (OP == kRaggedTN ? t.seg_rows : p.nc) : 0;
+        // (a quadrant may lie outside the segment or the matrix: it copies and stores nothing)
+        if constexpr (REST) t.nc = __builtin_amdgcn_readfirstlane(t.i0 < t.seg_rows && t.j0 < p.nj ? t.nc : 0);
         int c_first = 0;
         if constexpr (SLICED) {
             t.slice = __builtin_amdgcn_readfirstlane(slice);
@@ -420,7 +448,8 @@ ragged_gemm_kernel(const RaggedParams p) {
         uint8_t* const base = (uint8_t*)p.d + (OP == kRaggedTN ? (long)t.g * p.d_gstride + (long)t.i0 * p.ldd
                                                                : (long)(t.seg0 + t.i0) * p.ldd) * D_SIZE
                               + (SLICED ? t.slice * p.slice_stride * 4 : 0);
-        const int rows = min((OP == kRaggedTN ? p.ni : t.seg_rows) - t.i0, BM);
+        int rows = min((OP == kRaggedTN ? p.ni : t.seg_rows) - t.i0, BM);
+        if constexpr (REST) rows = __builtin_amdgcn_readfirstlane(max(rows, 0));
         return buffer_over(base, some ? rows * (int)p.ldd * D_SIZE : 0);
     };
     const bool add = OP == kRaggedTN && p.accumulate;
@@ -548,7 +577,7 @@ ragged_few_rows_kernel(const RaggedParams p) {
     const int l16 = lane & 15, lgrp = lane >> 4;
     if (wave == 0) {
         read_segments(p, lane, s_off);
-        count_row_tiles<16>(p.groups, lane, s_off, s_tiles);
+        count_row_tiles(16, p.groups, lane, s_off, s_tiles);
     }
     __syncthreads();
     const int total = __builtin_amdgcn_readfirstlane(s_tiles[p.groups]) * p.tiles_j;

@@ -25,6 +25,10 @@ struct RaggedParams {
     int accumulate;          // tn: add to what D holds
     int slices;              // > 1: the contraction is cut into as many parts, whose fp32 sums
     long slice_stride;       // go to D + part * slice_stride (a workspace) and are joined later
+    // nt, nn, > 0: a pair of launches shares the work.  The 256x256 kernel, whose grid this is,
+    // leaves out its last round where that fills at most half of the grid; the 128x128
+    // kernel then takes the quadrants of those tiles (its tiles_j counts 256 columns each).
+    int cut;
 };
 
 // The join: D = [D +] the sum of the slices, in their order.  D is [rows][width] of the type

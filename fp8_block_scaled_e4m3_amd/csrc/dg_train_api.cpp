@@ -20,6 +20,7 @@ namespace {
 constexpr int kMaxConfigs = 64;
 constexpr long kMaxLd = 1l << 21;      // a tile is addressed with 31-bit offsets: 256 rows of ld fp32 values
 constexpr long kMaxWorkspace = 256l << 20;   // what dg_ragged_workspace_bytes asks for at most
+constexpr int kLeastCut = 2048;        // (see shares_last_round)
 constexpr long kMaxTiles = 1l << 30;   // tile numbers, and one round past the last, are ints
 
 // dg_set_ragged_tile: 0 plans.  Per thread, like dg_set_kernel_config.
@@ -76,6 +77,19 @@ long elements_of_d(int op, const dg::RaggedParams& p) {
     return (op == dg::kRaggedTN ? (long)p.groups * p.ni : (long)p.rows) * p.nj;
 }
 
+// Whether the last round of 256x256 tiles, where it is short, goes to a second launch of 128x128
+// tiles (RaggedParams::cut; the same sums in the same order).  That launch costs 4 us also where
+// the device finds nothing for it, and at most about half a round is won:
+// n 4096, rounds (us without -> with)   0.7        1.5        2.25       2.6        4.25
+//   nc 1024                           29 -> 33   58 -> 56   85 -> 79   83 -> 93   140 -> 132
+//   nc 2048                           48 -> 52  102 -> 92  149 -> 131 150 -> 155  242 -> 229
+//   nc 7168                          139 -> 143 326 -> 276 479 -> 408 489 -> 497  818 -> 774
+// (over eight rounds 1%: with all CUs at work for longer, power takes the clock down, and a last
+// round of few tiles runs faster.)
+bool shares_last_round(int op, const dg::RaggedParams& p, const dg::RaggedConfig& c, int cus) {
+    return op != dg::kRaggedTN && c.bm == 256 && p.nc >= kLeastCut && tiles_expected(op, p, c.bm, c.bn) > cus;
+}
+
 // Expected time (us) of a configuration with `slots` workgroups at a time on `cus` CUs and the
 // contraction cut into `slices`.
 double time_expected(int op, const dg::RaggedParams& p, const dg::RaggedConfig& c, int cus, int slots, int slices) {
@@ -90,7 +104,7 @@ double time_expected(int op, const dg::RaggedParams& p, const dg::RaggedConfig& 
     }
     double rounds = tiles / slots;
     // part of a round takes a round's time (over many rounds it evens out)
-    if (rounds < 2) rounds = rounds <= 1.04 ? 1 : 2;
+    if (rounds < 2) rounds = rounds <= 1.04 ? 1 : rounds <= 1.45 && shares_last_round(op, p, c, cus) ? 1.7 : 2;
     const double step = tiles <= cus ? c.single_time + (c.each_time - c.single_time) * tiles / cus : c.round_time * rounds;
     const double time = step * steps + rounds * c.tile_time;
     // the join: a launch and its share of the call, the sums written and read at about 4 TB/s
@@ -173,7 +187,18 @@ int launch_ragged(int op, int half, int out_f32, dg::RaggedParams& p, void* work
         p.ldd = p.nj;
         p.accumulate = 0;
     }
+    const dg::RaggedConfig* rest = nullptr;
+    long rest_grid = 0;
+    if (shares_last_round(op, p, c, cus)) {
+        for (int i = 0; i < count && !rest; ++i)
+            if (cfgs[i].op == op && cfgs[i].half == half && !cfgs[i].out_f32 && cfgs[i].bm == 128 && cfgs[i].bn == 128) {
+                rest = &cfgs[i];
+                rest_grid = (long)units * blocks_per_cu(rest, i);
+            }
+        if (rest) p.cut = (int)grid;
+    }
     if (c.launch(p, (int)grid, static_cast<hipStream_t>(stream)) != hipSuccess ||
+        (rest && rest->launch(p, (int)rest_grid, static_cast<hipStream_t>(stream)) != hipSuccess) ||
         (plan.slices > 1 && dg::launch_ragged_join(join, static_cast<hipStream_t>(stream)) != hipSuccess)) {
         (void)hipGetLastError();
         return DG_ERR_HIP;
