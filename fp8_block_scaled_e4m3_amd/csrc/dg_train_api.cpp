@@ -84,10 +84,13 @@ long elements_of_d(int op, const dg::RaggedParams& p) {
 //   nc 1024                           29 -> 33   58 -> 56   85 -> 79   83 -> 93   140 -> 132
 //   nc 2048                           48 -> 52  102 -> 92  149 -> 131 150 -> 155  242 -> 229
 //   nc 7168                          139 -> 143 326 -> 276 479 -> 408 489 -> 497  818 -> 774
-// (over eight rounds 1%: with all CUs at work for longer, power takes the clock down, and a last
-// round of few tiles runs faster.)
+// Eight skewed groups, nc 7168: 1.2 rounds 326 -> 284 us, 2.2 484 -> 450, 4.2 816 -> 803, 8.25 1492 ->
+// 1482; input gradient of 7.3 and 9.1 rounds 777 -> 781, 958 -> 964.  (With all CUs at work for
+// longer, power takes the clock down, and a last round of few tiles runs faster.)
 bool shares_last_round(int op, const dg::RaggedParams& p, const dg::RaggedConfig& c, int cus) {
-    return op != dg::kRaggedTN && c.bm == 256 && p.nc >= kLeastCut && tiles_expected(op, p, c.bm, c.bn) > cus;
+    if (op == dg::kRaggedTN || c.bm != 256 || p.nc < kLeastCut) return false;
+    const double rounds = tiles_expected(op, p, c.bm, c.bn) / cus;
+    return rounds > 1 && rounds < 6;
 }
 
 // Expected time (us) of a configuration with `slots` workgroups at a time on `cus` CUs and the
