@@ -32,8 +32,10 @@
 // dealt out between the products (1209), tiles that follow one another without a break
 // (1323).  Tried without gain: raised wave priority around the products (-1%), bands of 4 and 16
 // (-0.5%, -1%), stores of D that bypass L2 (-1.5%), copies in the first half of the rows
-// (-2%), reads spread over half or all of the rows (-0.5%), four waves of 128x128 with
-// accumulators in AGPRs (the compiler moves them through VGPRs in the loop), a ring of four
+// (-2%), one to three of a step's copies held back to the next half (-2 to -5%), reads spread over
+// half or all of the rows (-0.5%), four waves of 128x128 with the accumulators pinned to AGPRs
+// (a third fewer LDS reads; forward 1394 to 1439 for 1432 to 1443, however its copies and reads
+// are dealt out), other row pitches (6912 to 7424 c: within 1%), a ring of four
 // stages of 32 c (-12%, input gradient -7%, weight gradient -4%: a barrier costs 4% of 64 c, and
 // the copies' latency is covered already).
 #include "dg_device.h"
