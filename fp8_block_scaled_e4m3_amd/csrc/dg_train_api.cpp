@@ -65,12 +65,13 @@ int blocks_per_cu(const dg::RaggedConfig* c, int index) {
 
 // Expected tiles of D, for the choice of a tile.  The split of the rows over the groups is on the
 // device: with many rows a group wastes half a row tile on average, with few each group
-// has one, and the longer ones a few more.
+// has one, and the longer ones a few more.  (Whole row tiles: 16 groups of few rows times 32 columns
+// are 512 tiles, one round, and not a little more.)
 double tiles_expected(int op, const dg::RaggedParams& p, int bm, int bn) {
     const double columns = (double)ceil_div(p.nj, bn);
     if (op == dg::kRaggedTN) return (double)p.groups * ceil_div(p.ni, bm) * columns;
     const double filled = p.groups < p.rows ? p.groups : p.rows, whole = (double)p.rows / bm;
-    return (whole >= filled ? whole + 0.5 * filled : filled + 0.25 * whole) * columns;
+    return std::floor((whole >= filled ? whole + 0.5 * filled : filled + 0.25 * whole) + 0.5) * columns;
 }
 
 long elements_of_d(int op, const dg::RaggedParams& p) {
@@ -106,8 +107,9 @@ double time_expected(int op, const dg::RaggedParams& p, const dg::RaggedConfig& 
         return (step > c.single_time ? step : c.single_time) * steps + c.tile_time;
     }
     double rounds = tiles / slots;
-    // part of a round takes a round's time (over many rounds it evens out)
-    if (rounds < 2) rounds = rounds <= 1.04 ? 1 : rounds <= 1.45 && shares_last_round(op, p, c, cus) ? 1.7 : 2;
+    // part of a round takes a round's time (over many rounds it evens out), from the first tile past
+    // the round on: 2676 rows, 2 groups, 2960 x 4056 are 528 tiles of 128x128, 119 us (256x256: 86)
+    if (rounds < 2) rounds = rounds <= 1 ? 1 : rounds <= 1.45 && shares_last_round(op, p, c, cus) ? 1.7 : 2;
     const double step = tiles <= cus ? c.single_time + (c.each_time - c.single_time) * tiles / cus : c.round_time * rounds;
     const double time = step * steps + rounds * c.tile_time;
     // the join: a launch and its share of the call, the sums written and read at about 4 TB/s
